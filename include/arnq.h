@@ -92,10 +92,13 @@ typedef enum arnq_status {
   ARNQ_ERR_WORKSPACE = 8,       /* workspace NULL or smaller than arnq_workspace_size()    */
   ARNQ_ERR_CUDA = 9,            /* a CUDA call failed (launch, attribute, device query)    */
   ARNQ_ERR_PLAN = 10,           /* an explicit plan that cannot run this problem           */
-  ARNQ_ERR_DEVICE_TIMEOUT = 11  /* reported through the workspace status block only        */
+  ARNQ_ERR_DEVICE_TIMEOUT = 11, /* reported through the workspace status block only        */
+  ARNQ_ERR_ARG = 12             /* an attribute out of range: activation, residual scale,
+                                   rows of the gate                                        */
 } arnq_status;
 
-typedef enum arnq_dtype { ARNQ_BF16 = 0, ARNQ_FP16 = 1 } arnq_dtype;
+/* ARNQ_FP32 only as the output type of arnq_quant_matmul. */
+typedef enum arnq_dtype { ARNQ_BF16 = 0, ARNQ_FP16 = 1, ARNQ_FP32 = 2 } arnq_dtype;
 /* Code types of y1 and y2 ("aclnnAddRmsNormDynamicQuantV2", Formula: y1Out is
  * INT8 or INT4; the page fixes no INT4 container):
  *   ARNQ_INT8        int8 [rows, n]
@@ -106,7 +109,13 @@ typedef enum arnq_dtype { ARNQ_BF16 = 0, ARNQ_FP16 = 1 } arnq_dtype;
  *                    multiple of 8; y 4-byte aligned).  On a little-endian
  *                    device its bytes are those of ARNQ_INT4.
  * INT4 codes are two's-complement nibbles in [-7, 7]. */
-typedef enum arnq_qdtype { ARNQ_INT8 = 0, ARNQ_INT4 = 1, ARNQ_INT4_INT32 = 2 } arnq_qdtype;
+typedef enum arnq_qdtype {
+  ARNQ_INT8 = 0,
+  ARNQ_INT4 = 1,
+  ARNQ_INT4_INT32 = 2,
+  ARNQ_NO_CODES = 16 /* arnq_post_norm_add_rms_norm_dynamic_quant only: no codes and no scale,
+                        the normalised row rounded to dtype, [rows, n]                       */
+} arnq_qdtype;
 
 /* outputMask encoding: ARNQ_MASK_ABSENT means "outputMaskOptional not given";
  * otherwise bit 0 is outputMask[0] (y1) and bit 1 is outputMask[1] (y2). */
@@ -182,6 +191,67 @@ ARNQ_API arnq_status arnq_rms_norm_dynamic_quant(const void *x, const void *gamm
                                         arnq_dtype dt, float eps, arnq_qdtype qdt, void *y,
                                         float *scale, void *workspace, size_t workspace_bytes,
                                         void *stream);
+
+/* ---- the operators around the quantized product --------------------------
+ *
+ * A block with INT8 weights runs, on this library's calls: a norm and
+ * quantizer (above, or the fused one below) -> arnq_quant_matmul -> ... ->
+ * arnq_glu_dynamic_quant -> arnq_quant_matmul -> the fused norms below, whose
+ * codes are the next product's input. */
+
+/* The norms around a block's residual, fused: the block's output h is
+ * normalised, gated, scaled and added to the residual stream x, and the sum is
+ * normalised for the next block and quantized:
+ *     p     = h / sqrt(mean(h^2) + eps_post) * gamma_post
+ *     x'    = round16( x + residual_scale * gate * p )      (written as x_out)
+ *     y     = x' / sqrt(mean(x'^2) + eps) * gamma + beta
+ *     input = y * smooth                                    (y, without smooth)
+ *     scale = row_max(|input|) / Q,  code = round(input / scale)
+ *   h, x           [rows, n] dtype   required
+ *   gamma_post     [n] dtype         required
+ *   gate           [gate_rows, n] dtype, optional (NULL = 1; gate_rows is then
+ *                  0).  gate_rows divides rows: row r of x takes row
+ *                  r / (rows / gate_rows) of gate, so gate_rows = 1 is a gate
+ *                  for each channel, one row for each sequence of equal length
+ *                  a gate for each sequence, gate_rows = rows one for each token
+ *   residual_scale finite
+ *   gamma          [n] dtype         required
+ *   beta, smooth   [n] dtype         optional (NULL = 0, 1)
+ *   eps_post, eps  finite and >= 0
+ *   qdt            code type of y, or ARNQ_NO_CODES: y [rows, n] dtype holds
+ *                  input rounded to dtype and scale is not written (may be NULL)
+ *   x_out          [rows, n] dtype, optional; may be x (in-place update)
+ * Conventions are those of arnq_run: x' is the value an fp64 evaluation gives,
+ * rounded once; the x' that was rounded is the one that is normalised; scale
+ * and codes are the fp64 evaluation's.  A row whose Rms is 0 (zeros, with
+ * eps 0) is normalised to zeros.  A row with a NaN among its inputs gets scale
+ * NaN, one with an infinity (and no NaN) scale infinity, both with codes 0.
+ * Deterministic; one launch; needs no workspace.
+ * ARNQ_ERR_ARG: residual_scale not finite, gate_rows < 0 or not dividing rows,
+ * or gate_rows == 0 with a gate or > 0 without. */
+ARNQ_API arnq_status arnq_post_norm_add_rms_norm_dynamic_quant(
+    const void *h, const void *x, const void *gamma_post, const void *gate, int64_t gate_rows,
+    float residual_scale, const void *gamma, const void *beta, const void *smooth, int64_t rows,
+    int64_t n, arnq_dtype dt, float eps_post, float eps, arnq_qdtype qdt, void *y, float *scale,
+    void *x_out, void *stream);
+
+typedef enum arnq_activation {
+  ARNQ_SILU = 0,     /* g / (1 + exp(-g))                                        */
+  ARNQ_GELU_TANH = 1 /* 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)))          */
+} arnq_activation;
+
+/* Gated activation, then dynamic quantization, of the rows of a product with
+ * gate and up projections side by side:
+ *     input = act(x[:, :n]) * x[:, n:] * smooth;  scale and codes as above
+ *   x       [rows, 2n] dtype   required
+ *   smooth  [n] dtype          optional (NULL = 1)
+ *   y       [rows, n] codes, scale [rows] binary32
+ * Scale and codes are those of an fp64 evaluation; rows with NaN or infinite
+ * values as above.  Deterministic; one launch; needs no workspace.
+ * ARNQ_ERR_ARG: unknown activation. */
+ARNQ_API arnq_status arnq_glu_dynamic_quant(const void *x, const void *smooth, int64_t rows,
+                                            int64_t n, arnq_dtype dt, arnq_activation act,
+                                            arnq_qdtype qdt, void *y, float *scale, void *stream);
 
 /* Status block at the start of the workspace.  code is 0 (ARNQ_OK) until a
  * kernel records an error (ARNQ_ERR_DEVICE_TIMEOUT);

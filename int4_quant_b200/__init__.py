@@ -4,6 +4,12 @@ The operator of the CANN page "aclnnAddRmsNormDynamicQuantV2" (and its
 no-add sibling "aclnnRmsNormDynamicQuant"), computed by the hand-written
 kernels of ``libarnq.so`` behind the C ABI in ``include/arnq.h``.
 
+Around it stand the operators that turn its codes into a block with INT8
+weights: ``quant_matmul`` (the product of codes, with token and channel
+scales), ``glu_dynamic_quant`` (gated activation + quantization) and
+``post_norm_add_rms_norm_dynamic_quant`` (the norms around the residual, gate
+and residual scale, + quantization).
+
 ``int4_quant_b200._abi`` is the ctypes binding (same names as the C entry
 points).  The functions below are the torch-facing calls: they allocate the
 outputs with torch and hand raw pointers to the library; every step of the
@@ -168,4 +174,156 @@ def rms_norm_dynamic_quant(x, gamma, beta=None, smooth=None, *, eps: float = 1e-
                                           _QDT[qdtype], y, scale, ws, ws.numel(), stream)
     if st != _abi.ARNQ_OK:
         raise ArnqError(st, "arnq_rms_norm_dynamic_quant")
+    return y, scale
+
+
+_ACT = {"silu": _abi.ARNQ_SILU, "gelu_tanh": _abi.ARNQ_GELU_TANH}
+
+
+def _operand(t, name, device, dtype, shape=None):
+    """Checks a tensor against the first one's device and a dtype (and shape)."""
+    _check(t, name, dtype)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _call(entry, args, device, stream, outputs, workspace_bytes=0):
+    """Allocates the outputs not given (on the stream the call runs on) and
+    calls a C entry point with the tensors' device current.
+
+    outputs: list of (given tensor or None, name, shape, dtype), or None for an output
+    that the call does not have; returns the output tensors.  `args` builds
+    the entry's arguments from (pointers of the outputs, workspace, stream)."""
+    import torch
+
+    def go():
+        made = []
+        for o in outputs:
+            if o is None:
+                made.append(None)
+                continue
+            given, name, shape, dtype = o
+            if given is not None:
+                _operand(given, name, device, dtype, shape)
+            else:
+                given = torch.empty(shape, dtype=dtype, device=device)
+            made.append(given)
+        ws = workspace(device, workspace_bytes, stream) if workspace_bytes else None
+        st = getattr(_abi, entry)(*args(made, ws, stream))
+        if st != _abi.ARNQ_OK:
+            raise ArnqError(st, entry)
+        return made
+
+    current = torch.cuda.current_device() == device.index
+    if stream is None:
+        if current:
+            stream = torch.cuda.current_stream(device)
+            return go()
+        with torch.cuda.device(device):
+            stream = torch.cuda.current_stream(device)
+            return go()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, not on {device}")
+    with torch.cuda.stream(stream):  # the device too; outputs belong to this stream
+        return go()
+
+
+def post_norm_add_rms_norm_dynamic_quant(h, x, gamma_post, gamma, beta=None, gate=None, smooth=None,
+                                         *, residual_scale: float = 1.0, eps: float = 1e-6,
+                                         eps_post: Optional[float] = None,
+                                         qdtype: Optional[str] = "int8", stream=None,
+                                         out: Optional[dict] = None):
+    """The norms around a block's residual, with gate and residual scale, and
+    the next product's quantization:
+
+        p     = h / sqrt(mean(h^2) + eps_post) * gamma_post
+        x_out = round16(x + residual_scale * gate * p)
+        in    = (x_out / sqrt(mean(x_out^2) + eps) * gamma + beta) * smooth
+        scale = rowmax|in| / Q,  y = round(in / scale)
+
+    h (the block's output), x (the residual stream): [..., n] bf16 or fp16;
+    gamma_post, gamma, beta, smooth: [n] same dtype.  gate: [n] (a gate for
+    each channel) or [g, n], where g divides the number of rows: consecutive
+    runs of rows/g rows share a row of it (g sequences of equal length, or one
+    row for each token).  Returns (y, scale, x_out); y as in
+    add_rms_norm_dynamic_quant, or with qdtype=None `in` rounded to the
+    inputs' dtype and scale None.  eps_post defaults to eps.  `out` may pass
+    preallocated tensors under the keys y, scale, x_out; x_out may be x.
+    """
+    _check(x, "x")
+    dt, device, n = x.dtype, x.device, x.shape[-1] if x.dim() else 0
+    code = _DT.get(str(dt))
+    if code is None:
+        raise ValueError(f"unsupported dtype {dt}")
+    rows = x.numel() // n if n else 0
+    _operand(h, "h", device, dt, x.shape)
+    for name, t in (("gamma_post", gamma_post), ("gamma", gamma)):
+        _operand(t, name, device, dt, (n,))
+    for name, t in (("beta", beta), ("smooth", smooth)):
+        if t is not None:
+            _operand(t, name, device, dt, (n,))
+    gate_rows = 0
+    if gate is not None:
+        _operand(gate, "gate", device, dt)
+        if gate.dim() < 1 or gate.shape[-1] != n:
+            raise ValueError(f"gate must have shape [{n}] or [g, {n}], got {tuple(gate.shape)}")
+        gate_rows = gate.numel() // n if n else 0
+    lead = tuple(x.shape[:-1])
+    if qdtype is None:
+        q, cshape, cdt = _abi.ARNQ_NO_CODES, tuple(x.shape), dt
+    else:
+        cshape, cdt = _codes_like(lead, n, qdtype)
+        q = _QDT[qdtype]
+    given = out or {}
+    import torch
+    y, scale, x_out = _call(
+        "arnq_post_norm_add_rms_norm_dynamic_quant",
+        lambda o, ws, st: (h, x, gamma_post, gate, gate_rows, residual_scale, gamma, beta, smooth,
+                           rows, n, code, eps if eps_post is None else eps_post, eps, q, o[0],
+                           o[1], o[2], st),
+        device, stream,
+        [(given.get("y"), "y", cshape, cdt),
+         None if qdtype is None else (given.get("scale"), "scale", lead, torch.float32),
+         (given.get("x_out"), "x_out", tuple(x.shape), dt)])
+    return y, scale, x_out
+
+
+def glu_dynamic_quant(x, smooth=None, *, activation: str = "silu", qdtype: str = "int8",
+                      stream=None, out: Optional[dict] = None):
+    """Gated activation and quantization of a product's rows, gate and up
+    projections side by side:
+
+        in = act(x[..., :n]) * x[..., n:] * smooth
+        scale = rowmax|in| / Q,  y = round(in / scale)
+
+    x: [..., 2n] bf16 or fp16; smooth: [n] same dtype; activation "silu" or
+    "gelu_tanh".  Returns (y, scale); `out` may pass them preallocated.
+    """
+    _check(x, "x")
+    dt, device = x.dtype, x.device
+    code = _DT.get(str(dt))
+    if code is None:
+        raise ValueError(f"unsupported dtype {dt}")
+    if activation not in _ACT:
+        raise ValueError(f"unknown activation {activation!r}")
+    two_n = x.shape[-1] if x.dim() else 0
+    if two_n % 2:
+        raise ValueError(f"x must have an even last dimension (gate and up), got {two_n}")
+    n = two_n // 2
+    rows = x.numel() // two_n if n else 0
+    if smooth is not None:
+        _operand(smooth, "smooth", device, dt, (n,))
+    lead = tuple(x.shape[:-1])
+    cshape, cdt = _codes_like(lead, n, qdtype)
+    given = out or {}
+    import torch
+    y, scale = _call(
+        "arnq_glu_dynamic_quant",
+        lambda o, ws, st: (x, smooth, rows, n, code, _ACT[activation], _QDT[qdtype], o[0], o[1], st),
+        device, stream,
+        [(given.get("y"), "y", cshape, cdt), (given.get("scale"), "scale", lead, torch.float32)])
     return y, scale

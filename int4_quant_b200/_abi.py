@@ -32,9 +32,12 @@ ARNQ_ERR_WORKSPACE = 8
 ARNQ_ERR_CUDA = 9
 ARNQ_ERR_PLAN = 10
 ARNQ_ERR_DEVICE_TIMEOUT = 11
+ARNQ_ERR_ARG = 12
 
-ARNQ_BF16, ARNQ_FP16 = 0, 1
+ARNQ_BF16, ARNQ_FP16, ARNQ_FP32 = 0, 1, 2
 ARNQ_INT8, ARNQ_INT4, ARNQ_INT4_INT32 = 0, 1, 2
+ARNQ_NO_CODES = 16
+ARNQ_SILU, ARNQ_GELU_TANH = 0, 1
 ARNQ_MASK_ABSENT = -1
 ARNQ_MASK_Y1, ARNQ_MASK_Y2 = 1, 2
 ARNQ_MAX_N = 131072
@@ -84,6 +87,10 @@ _SIGS = {
                           _p, _p, _p, _sz, _p, _p], _i32),
     "arnq_run_static_scratch": ([_p, _p, _p, _p, _p, _p, _i64, _i64, _i32, _f32, _i32, _i32, _p, _p,
                                  _p, _p, _p, _p], _i32),
+    "arnq_post_norm_add_rms_norm_dynamic_quant": (
+        [_p, _p, _p, _p, _i64, _f32, _p, _p, _p, _i64, _i64, _i32, _f32, _f32, _i32, _p, _p, _p,
+         _p], _i32),
+    "arnq_glu_dynamic_quant": ([_p, _p, _i64, _i64, _i32, _i32, _i32, _p, _p, _p], _i32),
 }
 
 
@@ -210,3 +217,18 @@ def arnq_run_static_scratch(x1, x2, gamma, beta, smooth1, smooth2, rows, n, dt, 
                                          float(eps), int(out_mask), int(qdt), _ptr(y1),
                                          _ptr(scale1), _ptr(y2), _ptr(scale2), _ptr(x_out),
                                          _stream(stream))
+
+
+def arnq_post_norm_add_rms_norm_dynamic_quant(h, x, gamma_post, gate, gate_rows, residual_scale,
+                                              gamma, beta, smooth, rows, n, dt, eps_post, eps,
+                                              qdt, y, scale, x_out, stream) -> int:
+    return lib().arnq_post_norm_add_rms_norm_dynamic_quant(
+        _ptr(h), _ptr(x), _ptr(gamma_post), _ptr(gate), int(gate_rows), float(residual_scale),
+        _ptr(gamma), _ptr(beta), _ptr(smooth), int(rows), int(n), int(dt), float(eps_post),
+        float(eps), int(qdt), _ptr(y), _ptr(scale), _ptr(x_out), _stream(stream))
+
+
+def arnq_glu_dynamic_quant(x, smooth, rows, n, dt, act, qdt, y, scale, stream) -> int:
+    return lib().arnq_glu_dynamic_quant(_ptr(x), _ptr(smooth), int(rows), int(n), int(dt),
+                                        int(act), int(qdt), _ptr(y), _ptr(scale),
+                                        _stream(stream))

@@ -727,6 +727,7 @@ const char *arnq_status_string(arnq_status s) {
     case ARNQ_ERR_WORKSPACE: return "ARNQ_ERR_WORKSPACE: workspace missing or too small";
     case ARNQ_ERR_CUDA: return "ARNQ_ERR_CUDA: a CUDA call failed";
     case ARNQ_ERR_PLAN: return "ARNQ_ERR_PLAN: the launch plan cannot run this problem";
+    case ARNQ_ERR_ARG: return "ARNQ_ERR_ARG: an attribute is out of range";
     case ARNQ_ERR_DEVICE_TIMEOUT: return "ARNQ_ERR_DEVICE_TIMEOUT: a kernel gave up waiting for a copy";
   }
   return "ARNQ: unknown status";
