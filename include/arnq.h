@@ -199,6 +199,29 @@ ARNQ_API arnq_status arnq_rms_norm_dynamic_quant(const void *x, const void *gamm
  * arnq_glu_dynamic_quant -> arnq_quant_matmul -> the fused norms below, whose
  * codes are the next product's input. */
 
+/* Largest inner length of arnq_quant_matmul: the sums stay below 2^31. */
+#define ARNQ_MAX_K 131071
+
+/* Product of INT8 codes with a scale for each token and each channel:
+ *     y[t, c] = round( (sum_k x[t, k] * w[c, k]) * scale_x[t] * scale_w[c] + bias[c] )
+ *   x        [m, k] int8      required (codes in [-128, 127])
+ *   scale_x  [m] binary32     required
+ *   w        [n, k] int8      required: a weight's rows are its output channels
+ *   scale_w  [n] binary32     required
+ *   bias     [n] out_dt       optional (NULL = 0)
+ *   y        [m, n] out_dt (ARNQ_BF16, ARNQ_FP16 or ARNQ_FP32)
+ * with n <= ARNQ_MAX_N, k <= ARNQ_MAX_K.  The sum is exact (32-bit integers);
+ * it is converted to binary32, scaled and added to in binary32 and rounded once
+ * to out_dt (a scale that is NaN or infinite gives what binary32 gives).
+ * Deterministic; one launch.  Codes of any alignment are taken; tensor-map
+ * copies need k and both code pointers to be multiples of 16.
+ * workspace: arnq_workspace_size()'s 256 bytes, status block zero-filled once;
+ * written only if a bounded wait expires (ARNQ_ERR_DEVICE_TIMEOUT, row -1). */
+ARNQ_API arnq_status arnq_quant_matmul(const void *x, const float *scale_x, const void *w,
+                                       const float *scale_w, const void *bias, int64_t m, int64_t n,
+                                       int64_t k, arnq_dtype out_dt, void *y, void *workspace,
+                                       size_t workspace_bytes, void *stream);
+
 /* The norms around a block's residual, fused: the block's output h is
  * normalised, gated, scaled and added to the residual stream x, and the sum is
  * normalised for the next block and quantized:

@@ -232,6 +232,45 @@ def _call(entry, args, device, stream, outputs, workspace_bytes=0):
         return go()
 
 
+_OUT = {"torch.bfloat16": _abi.ARNQ_BF16, "torch.float16": _abi.ARNQ_FP16,
+        "torch.float32": _abi.ARNQ_FP32}
+
+
+def quant_matmul(x, scale_x, w, scale_w, bias=None, *, out_dtype=None, stream=None, out=None):
+    """Product of INT8 codes with a scale for each token and each channel:
+
+        y[..., c] = round((sum_k x[..., k] w[c, k]) * scale_x[...] * scale_w[c] + bias[c])
+
+    x: [..., k] int8 and scale_x: [...] float32, as the quantizers return
+    them; w: [n, k] int8 (rows are output channels) and scale_w: [n] float32;
+    bias: [n] of the output dtype.  out_dtype: torch.bfloat16 (the default),
+    float16 or float32; `out` may pass y [..., n] preallocated.
+    """
+    import torch
+    _check(x, "x", torch.int8)
+    device = x.device
+    if out_dtype is None:
+        out_dtype = torch.bfloat16
+    code = _OUT.get(str(out_dtype))
+    if code is None:
+        raise ValueError(f"unsupported out_dtype {out_dtype}")
+    lead, k = tuple(x.shape[:-1]), x.shape[-1] if x.dim() else 0
+    _operand(w, "w", device, torch.int8)
+    if w.dim() != 2 or w.shape[1] != k:
+        raise ValueError(f"w must have shape [n, {k}], got {tuple(w.shape)}")
+    n = w.shape[0]
+    m = x.numel() // k if k else 0
+    _operand(scale_x, "scale_x", device, torch.float32, lead)
+    _operand(scale_w, "scale_w", device, torch.float32, (n,))
+    if bias is not None:
+        _operand(bias, "bias", device, out_dtype, (n,))
+    return _call(
+        "arnq_quant_matmul",
+        lambda o, ws, st: (x, scale_x, w, scale_w, bias, m, n, k, code, o[0], ws, ws.numel(), st),
+        device, stream, [(out, "out", lead + (n,), out_dtype)],
+        workspace_bytes=_abi.ARNQ_WORKSPACE_BYTES)[0]
+
+
 def post_norm_add_rms_norm_dynamic_quant(h, x, gamma_post, gamma, beta=None, gate=None, smooth=None,
                                          *, residual_scale: float = 1.0, eps: float = 1e-6,
                                          eps_post: Optional[float] = None,

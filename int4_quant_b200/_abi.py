@@ -41,6 +41,7 @@ ARNQ_SILU, ARNQ_GELU_TANH = 0, 1
 ARNQ_MASK_ABSENT = -1
 ARNQ_MASK_Y1, ARNQ_MASK_Y2 = 1, 2
 ARNQ_MAX_N = 131072
+ARNQ_MAX_K = 131071
 
 ARNQ_KERNEL_AUTO, ARNQ_KERNEL_DIRECT, ARNQ_KERNEL_STAGED = 0, 1, 2
 ARNQ_STATIC_SCRATCH_BYTES = 4096
@@ -87,6 +88,7 @@ _SIGS = {
                           _p, _p, _p, _sz, _p, _p], _i32),
     "arnq_run_static_scratch": ([_p, _p, _p, _p, _p, _p, _i64, _i64, _i32, _f32, _i32, _i32, _p, _p,
                                  _p, _p, _p, _p], _i32),
+    "arnq_quant_matmul": ([_p, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _p, _sz, _p], _i32),
     "arnq_post_norm_add_rms_norm_dynamic_quant": (
         [_p, _p, _p, _p, _i64, _f32, _p, _p, _p, _i64, _i64, _i32, _f32, _f32, _i32, _p, _p, _p,
          _p], _i32),
@@ -232,3 +234,10 @@ def arnq_glu_dynamic_quant(x, smooth, rows, n, dt, act, qdt, y, scale, stream) -
     return lib().arnq_glu_dynamic_quant(_ptr(x), _ptr(smooth), int(rows), int(n), int(dt),
                                         int(act), int(qdt), _ptr(y), _ptr(scale),
                                         _stream(stream))
+
+
+def arnq_quant_matmul(x, scale_x, w, scale_w, bias, m, n, k, out_dt, y, workspace, workspace_bytes,
+                      stream) -> int:
+    return lib().arnq_quant_matmul(_ptr(x), _ptr(scale_x), _ptr(w), _ptr(scale_w), _ptr(bias),
+                                   int(m), int(n), int(k), int(out_dt), _ptr(y), _ptr(workspace),
+                                   int(workspace_bytes), _stream(stream))

@@ -17,12 +17,13 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC_DIR = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(SRC_DIR, f) for f in ["arnq_api.cu", "arnq_host.cu", "arnq_norms.cu",
-                                              "arnq_glu.cu"] + [
+                                              "arnq_glu.cu", "arnq_matmul.cu"] + [
     f"arnq_k_{dt}_{q}{cl}.cu" for dt in ("bf16", "fp16") for q in ("int8", "int4")
     for cl in ("", "_cl")]]
 DEPS = SOURCES + [os.path.join(SRC_DIR, f) for f in (
     "arnq_kernels.cuh", "arnq_table.h", "arnq_host.h", "arnq_rowquant.cuh",
-    "arnq_rowquant_host.h", "arnq_norms.cuh", "arnq_glu.cuh")] + [
+    "arnq_rowquant_host.h", "arnq_norms.cuh", "arnq_glu.cuh", "arnq_tc.cuh",
+    "arnq_matmul.cuh")] + [
         os.path.join(ROOT, "include", "arnq.h")]
 LIB = os.path.join(PKG, "libarnq.so")
 OBJ_DIR = os.path.join(ROOT, "_build")

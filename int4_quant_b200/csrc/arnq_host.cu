@@ -63,11 +63,11 @@ arnq_status resident_ctas(const void *fn, int dev, int threads, int smem, int *p
   return ARNQ_OK;
 }
 
-arnq_status launch_dependent(const void *fn, int64_t grid, int threads, int smem, int cluster,
+arnq_status launch_dependent(const void *fn, dim3 grid, int threads, int smem, int cluster,
                              cudaStream_t stream, void *params) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;

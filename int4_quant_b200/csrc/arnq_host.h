@@ -24,7 +24,7 @@ arnq_status resident_ctas(const void *fn, int dev, int threads, int smem, int *p
 
 // Launches as a programmatic dependent of the preceding work on the stream,
 // in clusters of `cluster` CTAs.
-arnq_status launch_dependent(const void *fn, int64_t grid, int threads, int smem, int cluster,
+arnq_status launch_dependent(const void *fn, dim3 grid, int threads, int smem, int cluster,
                              cudaStream_t stream, void *params);
 
 }  // namespace arnq

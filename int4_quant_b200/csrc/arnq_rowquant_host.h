@@ -49,7 +49,8 @@ arnq_status launch_rows(typename Op::Params p, int threads, cudaStream_t stream)
   st = resident_ctas(fn, dev, threads, 0, &per_sm);
   if (st != ARNQ_OK) return st;
   const int64_t slots = static_cast<int64_t>(per_sm) * sms;
-  return launch_dependent(fn, p.out.rows < slots ? p.out.rows : slots, threads, 0, 1, stream, &p);
+  return launch_dependent(fn, dim3(static_cast<unsigned>(p.out.rows < slots ? p.out.rows : slots)),
+                          threads, 0, 1, stream, &p);
 }
 
 }  // namespace arnq

@@ -96,7 +96,44 @@ def test_glu_refusals(kw, expect):
     assert glu(**kw) == expect
 
 
+def matmul(**kw):
+    a = dict(x=P["x"], scale_x=P["sc"], w=P["w"], scale_w=P["sw"], bias=None, m=8, n=64, k=32,
+             out_dt=A.ARNQ_BF16, y=P["y"], workspace=P["ws"], workspace_bytes=256, stream=None)
+    a.update(kw)
+    return A.arnq_quant_matmul(**a)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(x=None), A.ARNQ_ERR_NULL_PTR),
+    (dict(scale_x=None), A.ARNQ_ERR_NULL_PTR),
+    (dict(w=None), A.ARNQ_ERR_NULL_PTR),
+    (dict(scale_w=None), A.ARNQ_ERR_NULL_PTR),
+    (dict(y=None), A.ARNQ_ERR_NULL_PTR),
+    (dict(m=0), A.ARNQ_ERR_EMPTY),
+    (dict(n=0), A.ARNQ_ERR_EMPTY),
+    (dict(k=0), A.ARNQ_ERR_EMPTY),
+    (dict(m=-1), A.ARNQ_ERR_SHAPE),
+    (dict(m=2 ** 31), A.ARNQ_ERR_SHAPE),
+    (dict(n=A.ARNQ_MAX_N + 1), A.ARNQ_ERR_SHAPE),
+    (dict(k=A.ARNQ_MAX_K + 1), A.ARNQ_ERR_SHAPE),
+    (dict(out_dt=3), A.ARNQ_ERR_DTYPE),
+    (dict(y=P["y"] + 1), A.ARNQ_ERR_ALIGN),
+    (dict(out_dt=A.ARNQ_FP32, y=P["y"] + 2), A.ARNQ_ERR_ALIGN),
+    (dict(bias=P["bias"] + 1), A.ARNQ_ERR_ALIGN),
+    (dict(scale_x=P["sc"] + 2), A.ARNQ_ERR_ALIGN),
+    (dict(scale_w=P["sw"] + 2), A.ARNQ_ERR_ALIGN),
+    (dict(workspace=None), A.ARNQ_ERR_WORKSPACE),
+    (dict(workspace_bytes=255), A.ARNQ_ERR_WORKSPACE),
+    (dict(workspace=P["ws"] + 4), A.ARNQ_ERR_ALIGN),
+])
+def test_matmul_refusals(kw, expect):
+    assert matmul(**kw) == expect
+
+
 def test_torch_calls_refuse_cpu_tensors():
+    codes = torch.zeros(4, 64, dtype=torch.int8)
+    with pytest.raises(ValueError):
+        lib.quant_matmul(codes, torch.zeros(4), codes, torch.zeros(4))
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     v = torch.zeros(64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):

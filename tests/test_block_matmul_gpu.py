@@ -1,0 +1,200 @@
+"""The INT8 product with token and channel scales on a GPU, against the sum in
+64 bits (exact: the products' sums stay below 2^53)."""
+import pytest
+import torch
+
+import int4_quant_b200 as lib
+from int4_quant_b200 import _abi as A
+from int4_quant_b200 import build as B
+from tests import _block_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _setup():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    B.build()
+    A.lib()
+    torch.cuda.set_device(0)
+
+
+def case(m, n, k, bias=None, seed=0, full=False):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    lim = 128 if full else 127
+    x = torch.randint(-lim, 128, (m, k), generator=g, device="cuda", dtype=torch.int8)
+    w = torch.randint(-lim, 128, (n, k), generator=g, device="cuda", dtype=torch.int8)
+    sx = torch.rand(m, generator=g, device="cuda") * 0.05 + 0.01
+    sw = torch.rand(n, generator=g, device="cuda") * 0.001 + 0.0002
+    b = None if bias is None else torch.randn(n, generator=g, device="cuda").to(bias)
+    return x, sx, w, sw, b
+
+
+def check(x, sx, w, sw, b, y, label=""):
+    """Binary32: the sum's conversion, two products and the addition round once
+    each (2^-24 of what they round), the output once more by half a step."""
+    acc = x.double() @ w.double().T
+    prod = acc * sx.double()[:, None] * sw.double()
+    ref = prod if b is None else prod + b.double()
+    half = torch.finfo(y.dtype).eps / 2
+    bound = prod.abs() * 3 * 2.0 ** -24 * 1.001 + ref.abs() * 2.0 ** -24 * 1.001
+    if y.dtype != torch.float32:
+        bound = bound + (ref.abs() + bound) * half + (2.0 ** -25 if y.dtype == torch.float16 else 0)
+    err = (y.double() - ref).abs()
+    bad = err > bound
+    assert not bad.any(), (label, int(bad.sum()), bad.nonzero()[:4].tolist(), float(err.max()))
+
+
+def run(m, n, k, out=torch.bfloat16, bias=False, seed=0, **kw):
+    c = case(m, n, k, out if bias else None, seed, **kw)
+    y = lib.quant_matmul(c[0], c[1], c[2], c[3], c[4], out_dtype=out)
+    check(*c, y, (m, n, k))
+
+
+@pytest.mark.parametrize("m,n,k", [(16, 128, 128), (1, 128, 128), (1, 8, 16), (16, 128, 512),
+                                   (7, 256, 1024), (32, 384, 4096), (256, 128, 256),
+                                   (200, 1000, 1040), (257, 520, 2064)])
+def test_small(m, n, k):
+    run(m, n, k, seed=m + n + k)
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("m,n,k", [(5, 260, 4096), (130, 514, 768), (600, 777, 528)])
+def test_types_and_bias(m, n, k, out, bias):
+    run(m, n, k, out, bias, seed=m)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 1, 1), (3, 5, 7), (17, 129, 127), (129, 1023, 1001),
+                                   (2, 64, 4099), (300, 130, 333)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_odd_sizes(m, n, k, out):
+    run(m, n, k, out, True, seed=n)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 4096, 4096), (4, 1024, 16384), (16, 16384, 1024),
+                                   (64, 5120, 5120), (512, 4096, 1024), (1111, 2048, 2048),
+                                   (4096, 4096, 512)])
+def test_ordinary_sizes(m, n, k):
+    run(m, n, k, seed=k)
+
+
+@pytest.mark.parametrize("k", [131071, 131056])
+def test_longest_sums(k):
+    # every code -128: the largest sum, 2^31 - 2^14 or below
+    x = torch.full((3, k), -128, dtype=torch.int8, device="cuda")
+    w = torch.full((130, k), -128, dtype=torch.int8, device="cuda")
+    w[1] = 127
+    sx = torch.ones(3, device="cuda")
+    sw = torch.ones(130, device="cuda")
+    check(x, sx, w, sw, None, lib.quant_matmul(x, sx, w, sw, out_dtype=torch.float32))
+
+
+def test_full_code_range():
+    run(33, 256, 1024, torch.float32, seed=1, full=True)
+
+
+@pytest.mark.parametrize("offset", [1, 4, 8])
+def test_misaligned_codes(offset):
+    x, sx, w, sw, _ = case(9, 130, 512, seed=offset)
+    bx = torch.empty(x.numel() + offset, dtype=torch.int8, device="cuda")
+    bw = torch.empty(w.numel() + offset, dtype=torch.int8, device="cuda")
+    bx[offset:].copy_(x.reshape(-1))
+    bw[offset:].copy_(w.reshape(-1))
+    x2, w2 = bx[offset:].view(x.shape), bw[offset:].view(w.shape)
+    y = lib.quant_matmul(x2, sx, w2, sw)
+    check(x, sx, w, sw, None, y)
+    assert torch.equal(y, lib.quant_matmul(x, sx, w, sw))
+
+
+def test_output_beside_others():
+    # an output that starts off a vector boundary, and canaries around it
+    x, sx, w, sw, _ = case(50, 200, 256, seed=3)
+    buf = torch.full((50 * 200 + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = buf[33:33 + 50 * 200].view(50, 200)
+    lib.quant_matmul(x, sx, w, sw, out=y)
+    check(x, sx, w, sw, None, y)
+    assert (buf[:33] == 7).all() and (buf[33 + 10000:] == 7).all()
+
+
+def test_scales_propagate():
+    x, sx, w, sw, _ = case(4, 128, 128, seed=5)
+    sx[0], sx[1], sx[2] = 0.0, float("nan"), float("inf")
+    y = lib.quant_matmul(x, sx, w, sw, out_dtype=torch.float32)
+    assert (y[0] == 0).all() and torch.isnan(y[1]).all() and not torch.isfinite(y[2]).any()
+    check(x[3:], sx[3:], w, sw, None, y[3:])
+
+
+def test_leading_dimensions_and_empty():
+    x, sx, w, sw, _ = case(12, 128, 64, seed=6)
+    y = lib.quant_matmul(x.view(3, 4, 64), sx.view(3, 4), w, sw)
+    assert y.shape == (3, 4, 128)
+    check(x, sx, w, sw, None, y.view(12, 128))
+    with pytest.raises(lib.ArnqError):
+        lib.quant_matmul(x[:0], sx[:0], w, sw)
+    with pytest.raises(ValueError):
+        lib.quant_matmul(x, sx, w[:, :32], sw)
+    with pytest.raises(ValueError):
+        lib.quant_matmul(x.t(), sx, w, sw)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 4096, 4096), (300, 512, 1024), (2048, 2048, 512), (9, 100, 99)])
+def test_deterministic_streams_and_graph(m, n, k):
+    x, sx, w, sw, _ = case(m, n, k, seed=7)
+    ref = lib.quant_matmul(x, sx, w, sw)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    a = lib.quant_matmul(x, sx, w, sw, stream=side)
+    b = lib.quant_matmul(x, sx, w, sw)
+    torch.cuda.synchronize()
+    assert torch.equal(ref, a) and torch.equal(ref, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = lib.quant_matmul(x, sx, w, sw)
+    y.zero_()
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(ref, y)
+
+
+def test_block_of_operators():
+    """A gated MLP with INT8 weights between its norms, as a model runs it, each
+    step against its 64-bit form on the step's own inputs."""
+    n, inner, rows = 512, 1024, 40
+    g = torch.Generator(device="cuda").manual_seed(9)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    t = torch.bfloat16
+    gamma = [(r(n) * 0.1 + 1).to(t) for _ in range(3)]
+    x1, x2 = r(rows, n).to(t), r(rows, n).to(t)
+    w1 = torch.randint(-127, 128, (2 * inner, n), generator=g, device="cuda", dtype=torch.int8)
+    w2 = torch.randint(-127, 128, (n, inner), generator=g, device="cuda", dtype=torch.int8)
+    sw1, sw2 = torch.full((2 * inner,), 0.001, device="cuda"), torch.full((n,), 0.001, device="cuda")
+    gate = r(4, n).to(t)
+
+    def block():
+        a, sa, _, _, x = lib.add_rms_norm_dynamic_quant(x1, x2, gamma[0])
+        gu = lib.quant_matmul(a, sa, w1, sw1)
+        b, sb = lib.glu_dynamic_quant(gu)
+        h = lib.quant_matmul(b, sb, w2, sw2)
+        y, sy, xo = lib.post_norm_add_rms_norm_dynamic_quant(h, x, gamma[1], gamma[2], gate=gate,
+                                                             residual_scale=0.5)
+        return a, sa, x, gu, b, sb, h, y, sy, xo
+
+    a, sa, x, gu, b, sb, h, y, sy, xo = got = block()
+    check(a, sa, w1, sw1, None, gu)
+    R.check_codes(b, sb, R.glu_in(gu.cpu(), None, "silu"), "int8")
+    check(b, sb, w2, sw2, None, h)
+    c = lambda v: v.cpu()  # noqa: E731
+    R.check_x(xo, R.norms_x(c(h), c(x), c(gamma[1]), c(gate), 0.5, 1e-6))
+    R.check_codes(y, sy, R.norms_in(c(xo), c(gamma[2]), None, None, 1e-6), "int8")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = block()
+    for v in again:
+        v.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    for p, q in zip(got, again):
+        assert torch.equal(p, q)
