@@ -9,6 +9,7 @@ template <class T, int ACT, int QT, bool VEC>
 arnq_status by_upt(const GluParams &p, int upt, int threads, cudaStream_t s) {
   if (upt == 1) return launch_rows<GluOp<T, ACT, QT, VEC, 1>>(p, threads, s);
   if (upt == 2) return launch_rows<GluOp<T, ACT, QT, VEC, 2>>(p, threads, s);
+  if (upt == 4) return launch_rows<GluOp<T, ACT, QT, VEC, 4>>(p, threads, s);
   return launch_rows<GluOp<T, ACT, QT, VEC, 0>>(p, threads, s);
 }
 template <class T, int ACT, int QT>
@@ -50,8 +51,10 @@ extern "C" arnq_status arnq_glu_dynamic_quant(const void *x, const void *smooth,
   const int qt = kernel_qt(qdt);
   const bool vec = n % 8 == 0 && is_aligned(x, 16) && is_aligned(smooth, 16) &&
                    is_aligned(y, qt == 0 ? 8 : 4);
-  int upt = 0, threads = 0;
-  row_threads(p.out.units, &upt, &threads);
+  int dev = 0, sms = 0, upt = 0, threads = 0;
+  st = current_device(&dev, &sms);
+  if (st != ARNQ_OK) return st;
+  row_threads(p.out.units, rows > sms, 512, &upt, &threads);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return dt == ARNQ_BF16 ? by_act<Bf16>(p, act, qt, vec, upt, threads, s)
                          : by_act<Fp16>(p, act, qt, vec, upt, threads, s);

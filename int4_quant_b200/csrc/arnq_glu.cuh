@@ -10,9 +10,11 @@
 // log2 e, the constants'), which the sigmoid passes on for z < 0 and weakens
 // to at most 0.28 * 6 for z > 0; the exponential (4), the division (4) and
 // the remaining roundings (3) add 11.  The quotient by the scale adds 3.
-// Altogether |error| <= |in| 2^-24 (20 + 8 max(-z, 0)) with a margin.  Values
-// with z < kLow, whose sigmoid nears the end of binary32's range, are
-// computed in fp64.
+// Altogether |error| <= |in| 2^-24 (20 + 8 max(-z, 0)) with a margin, for
+// z >= kLow.  Below that, where the sigmoid nears the end of binary32's range,
+// a value is at most 1.5e-33 |u smooth|: with |u smooth| <= 1e8 it and its
+// error are far below what a row's maximum of at least kTiny (1e-18) can tell
+// from zero; a row with a larger factor there is computed in fp64.
 #pragma once
 
 #include "arnq_rowquant.cuh"
@@ -29,85 +31,99 @@ struct GluParams {
   const uint16_t *smooth;  // [n] or nullptr
 };
 
+// one value in fp64: g[0], u = g[n]
+template <class T, int ACT>
+__device__ __noinline__ double glu64(const uint16_t *gate, int n, const uint16_t *smooth) {
+  const double g = static_cast<double>(Cvt<T>::f1(gate[0]));
+  const double t = static_cast<double>(Cvt<T>::f1(gate[n]));
+  if (g == 0.0 || t == 0.0) return __dmul_rn(g, t);  // (0 times an infinity or NaN is NaN)
+  double z = g;
+  if (ACT == ACT_GELU_TANH) z = 1.5957691216057308 * (g + 0.044715 * g * g * g);
+  const double in = g / (1.0 + exp(-z)) * t;
+  return smooth ? in * static_cast<double>(Cvt<T>::f1(smooth[0])) : in;
+}
+
 template <class T_, int ACT, int QT_, bool VEC_, int UPT_>
 struct GluOp {
   typedef T_ T;
   typedef GluParams Params;
-  static constexpr int QT = QT_, UPT = UPT_;
-  static constexpr bool VEC = VEC_;
-  static constexpr int kMaxThreads = UPT == 4 ? 512 : 1024, kMinCtas = 1;
-  struct Raw {
-    uint4 g, u;
+  static constexpr int QT = QT_, UPT = UPT_, kInputs = 2;
+  static constexpr bool VEC = VEC_, STAGED = VEC_ && UPT_ > 0;
+  static constexpr int kMaxThreads = UPT == 4 ? 512 : 1024, kMinCtas = UPT == 4 ? 2 : 1;
+  struct Keep {
+    float low;  // the unit's smallest z, at most 0
   };
   const Params &p;
   __device__ __forceinline__ explicit GluOp(const Params &q) : p(q) {}
   __device__ __forceinline__ void setup(RowSmem &, int, int, int) {}
-  __device__ __forceinline__ Raw fetch(int64_t row, int u) const {
-    const uint16_t *r = p.x + row * (2 * static_cast<int64_t>(p.out.n));
-    Raw w;
-    w.g = load_unit<VEC, UPT != 0>(r, u, p.out.n);
-    w.u = load_unit<VEC, UPT != 0>(r + p.out.n, u, p.out.n);
-    return w;
+  __device__ __forceinline__ const uint16_t *gate_of(int64_t row) const {
+    return p.x + row * (2 * static_cast<int64_t>(p.out.n));
   }
-  __device__ __forceinline__ Raw refetch(int64_t row, int u) const { return fetch(row, u); }
+  __device__ __forceinline__ void stage(int64_t row, int u, uint4 *slot, int stride) const {
+    const uint16_t *r = gate_of(row) + 8 * u;
+    copy16_async(slot, r);
+    copy16_async(slot + stride, r + p.out.n);
+  }
   template <class E>
-  __device__ __forceinline__ void prepare(RowSmem &, int64_t, Raw *, E &&, int) {}
+  __device__ __forceinline__ void prepare(RowSmem &, int64_t, Keep *, const uint4 *, int, E &&, int) {}
 
-  static __device__ __forceinline__ float arg(float g) {
+  static __device__ __forceinline__ float2 arg2(float2 g) {
     if (ACT == ACT_SILU) return g;
     // 2 sqrt(2/pi) = 1.5957691..., times 0.044715 = 0.0713548...
-    return g * __fmaf_rn(0.07135481282839f * g, g, 1.59576912160573f);
+    const float2 c = make_float2(0.07135481282839f, 0.07135481282839f),
+                 d = make_float2(1.59576912160573f, 1.59576912160573f);
+    return __fmul2_rn(g, __ffma2_rn(__fmul2_rn(c, g), g, d));
   }
-  // g * sigmoid(z): exp(-z) = 2^(-z log2 e)
-  static __device__ __forceinline__ float act(float g, float z) {
+  static __device__ __forceinline__ float exp2_approx(float y) {
     float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.44269504088896f * z));
-    return __fdividef(g, 1.f + e);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));
+    return e;
   }
-  __device__ __forceinline__ void value(const Raw &w, int u, float2 v[4]) const {
+  static __device__ __forceinline__ float rcp_approx(float y) {
+    float e;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));
+    return e;
+  }
+  __device__ __forceinline__ bool value(int64_t row, int u, Keep &keep, const uint4 *slot, int stride,
+                                        float2 v[4]) const {
     float2 g[4], t[4];
-    unpack<T>(w.g, g);
-    unpack<T>(w.u, t);
-    float low = 0.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float zx = arg(g[k].x), zy = arg(g[k].y);
-      low = fminf(low, fminf(zx, zy));
-      v[k] = __fmul2_rn(make_float2(act(g[k].x, zx), act(g[k].y, zy)), t[k]);
+    if (STAGED) {
+      unpack<T>(slot[0], g);
+      unpack<T>(slot[stride], t);
+    } else {
+      unpack<T>(load_unit<VEC, false>(gate_of(row), u, p.out.n), g);
+      unpack<T>(load_unit<VEC, false>(gate_of(row) + p.out.n, u, p.out.n), t);
     }
     if (p.smooth) {
       float2 s[4];
       unpack<T>(load_unit<VEC, false>(p.smooth, u, p.out.n), s);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = __fmul2_rn(v[k], s[k]);
+      for (int k = 0; k < 4; ++k) t[k] = __fmul2_rn(t[k], s[k]);  // exact
     }
-    if (low < kLow) {  // sigmoids near or below the end of binary32's range
-      const int cnt = min(8, p.out.n - 8 * u);
+    float low = 0.f;
+    const float2 l = make_float2(-1.44269504088896f, -1.44269504088896f), one = make_float2(1.f, 1.f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (j >= cnt || !(arg(elem(g, j)) < kLow)) continue;
-        const float f = __double2float_rn(value64(w, u, j));
-        if (j & 1) v[j >> 1].y = f;
-        else v[j >> 1].x = f;
-      }
+    for (int k = 0; k < 4; ++k) {
+      // g * sigmoid(z) * u * smooth, exp(-z) = 2^(-z log2 e)
+      const float2 z = arg2(g[k]);
+      low = fminf(low, fminf(z.x, z.y));
+      const float2 y = __fmul2_rn(z, l);
+      const float2 e = __fadd2_rn(make_float2(exp2_approx(y.x), exp2_approx(y.y)), one);
+      v[k] = __fmul2_rn(__fmul2_rn(g[k], make_float2(rcp_approx(e.x), rcp_approx(e.y))), t[k]);
     }
+    keep.low = low;
+    // a sigmoid that nears or leaves binary32's range matters only beside a
+    // huge factor
+    return !(low < kLow) || abs_max8(t) <= 1e8f;
   }
-  __device__ __forceinline__ double value64(const Raw &w, int u, int j) const {
-    const double g = static_cast<double>(Cvt<T>::f1(get16(w.g, j)));
-    const double t = static_cast<double>(Cvt<T>::f1(get16(w.u, j)));
-    if (g == 0.0 || t == 0.0) return __dmul_rn(g, t);  // (0 times an infinity or NaN is NaN)
-    double z = g;
-    if (ACT == ACT_GELU_TANH) z = 1.5957691216057308 * (g + 0.044715 * g * g * g);
-    const double a = g / (1.0 + exp(-z));
-    double in = a * t;
-    if (p.smooth) in *= static_cast<double>(Cvt<T>::f1(p.smooth[8 * u + j]));
-    return in;
+  __device__ __forceinline__ double value64(int64_t row, int c) const {
+    return glu64<T, ACT>(gate_of(row) + c, p.out.n, p.smooth ? p.smooth + c : nullptr);
   }
   // candidates for the maximum: 2^-13 covers the error for every z >= kLow
   __device__ __forceinline__ float slack(float M) const { return M * 1.220703125e-4f; }
-  __device__ __forceinline__ float tolerance(const Raw &w, int j, float t, float) const {
-    const float z = arg(Cvt<T>::f1(get16(w.g, j)));
-    return fabsf(t) * __fmaf_rn(fmaxf(-z, 0.f), 4.76837158203125e-7f, 1.1920928955078125e-6f);
+  __device__ __forceinline__ float coarse(const Keep &keep, float) const {
+    return (QT == 1 ? 7.01f : 127.01f) *
+           __fmaf_rn(fminf(-keep.low, -kLow), 4.76837158203125e-7f, 1.1920928955078125e-6f);
   }
 };
 

@@ -10,6 +10,7 @@ template <class T, int QT, bool VEC>
 arnq_status by_upt(const NormsParams &p, int upt, int threads, cudaStream_t s) {
   if (upt == 1) return launch_rows<NormsOp<T, QT, VEC, 1>>(p, threads, s);
   if (upt == 2) return launch_rows<NormsOp<T, QT, VEC, 2>>(p, threads, s);
+  if (upt == 4) return launch_rows<NormsOp<T, QT, VEC, 4>>(p, threads, s);
   return launch_rows<NormsOp<T, QT, VEC, 0>>(p, threads, s);
 }
 template <class T, int QT>
@@ -67,8 +68,11 @@ extern "C" arnq_status arnq_post_norm_add_rms_norm_dynamic_quant(
   p.alpha = residual_scale;
   p.eps_post = eps_post;
   p.eps = eps;
-  int upt = 0, threads = 0;
-  row_threads(p.out.units, &upt, &threads);
+  p.inv_n = 1.0 / static_cast<double>(n);
+  int dev = 0, sms = 0, upt = 0, threads = 0;
+  st = current_device(&dev, &sms);
+  if (st != ARNQ_OK) return st;
+  row_threads(p.out.units, rows > sms, 384, &upt, &threads);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return dt == ARNQ_BF16 ? by_codes<Bf16>(p, qt, vec, upt, threads, s)
                          : by_codes<Fp16>(p, qt, vec, upt, threads, s);

@@ -23,6 +23,7 @@ struct NormsParams {
   uint16_t *x_out;        // may be x; may be nullptr
   int32_t rows_per_gate;  // rows that share a row of gate; rows: one gate row for all
   float alpha, eps_post, eps;
+  double inv_n;           // 1 / n
 };
 
 // 1/Rms of a row in fp64, and in binary32 times `alpha`; ss >= 0 or NaN.
@@ -40,8 +41,8 @@ __device__ __forceinline__ Rms make_rms(double ss, double inv_n, float eps, floa
   const double ms = __fma_rn(ss, inv_n, static_cast<double>(eps));
   if (cold || !(ms >= 1e-30)) {
     // a zero Rms normalises a row of zeros: its values stay zero
-    const double rms = __dsqrt_rn(ms);
-    r.inv64 = rms == 0.0 ? 0.0 : __ddiv_rn(static_cast<double>(alpha), rms);
+    const double rms = sqrt_ieee(ms);
+    r.inv64 = rms == 0.0 ? 0.0 : div_ieee(static_cast<double>(alpha), rms);
     cold = true;
   } else {
     r.inv64 = __dmul_rn(static_cast<double>(alpha), rsqrt64(ms));
@@ -53,33 +54,68 @@ __device__ __forceinline__ Rms make_rms(double ss, double inv_n, float eps, floa
   return r;
 }
 
+// x' of one element in fp64, rounded once
+template <class T>
+__device__ __forceinline__ uint16_t x64(uint16_t h, uint16_t x, const uint16_t *gamma_post,
+                                        const uint16_t *gate, double inv) {
+  double t = __dmul_rn(__dmul_rn(static_cast<double>(Cvt<T>::f1(h)), inv),
+                       static_cast<double>(Cvt<T>::f1(*gamma_post)));
+  if (gate) t = __dmul_rn(t, static_cast<double>(Cvt<T>::f1(*gate)));
+  return round16<T>(__dadd_rn(static_cast<double>(Cvt<T>::f1(x)), t));
+}
+// The elements of a unit whose halves differ between lo and hi (the bound's two
+// ends), from the unit's inputs h and x; `count` elements exist.
+template <class T>
+__device__ __noinline__ uint4 settle_x(uint4 lo, uint4 hi, uint4 h, uint4 x, const uint16_t *gamma_post,
+                                       const uint16_t *gate, double inv, int count) {
+#pragma unroll 1
+  for (int j = 0; j < 8; ++j) {
+    if (get16(lo, j) == get16(hi, j)) continue;
+    set16(lo, j, j < count ? x64<T>(get16(h, j), get16(x, j), gamma_post + j, gate ? gate + j : nullptr, inv)
+                           : static_cast<uint16_t>(0));
+  }
+  return lo;
+}
+// This thread's part of a row's sum of squares in fp64 throughout: of row a or,
+// where x' was not stored, of x' made from h, x.
+template <class T>
+__device__ __noinline__ double sumsq_cold(const uint16_t *a, const uint16_t *h, const uint16_t *x,
+                                          const uint16_t *gamma_post, const uint16_t *gate, double inv,
+                                          int n) {
+  double s = 0.0;
+  for (int c = threadIdx.x; c < n; c += blockDim.x) {
+    const uint16_t w = a ? a[c] : x64<T>(h[c], x[c], gamma_post + c, gate ? gate + c : nullptr, inv);
+    const double v = static_cast<double>(Cvt<T>::f1(w));
+    s = __fma_rn(v, v, s);
+  }
+  return s;
+}
+
 template <class T_, int QT_, bool VEC_, int UPT_>
 struct NormsOp {
   typedef T_ T;
   typedef NormsParams Params;
-  static constexpr int QT = QT_, UPT = UPT_;
-  static constexpr bool VEC = VEC_;
-  static constexpr int kMaxThreads = UPT == 4 ? 512 : 1024, kMinCtas = 1;
-  struct Raw {
-    uint4 h, x;  // after prepare(): x holds x'
+  static constexpr int QT = QT_, UPT = UPT_, kInputs = 2;
+  static constexpr bool VEC = VEC_, STAGED = VEC_ && UPT_ > 0;
+  static constexpr int kMaxThreads = UPT == 4 ? 384 : 1024, kMinCtas = UPT == 4 ? 2 : 1;
+  struct Keep {
+    uint4 x;  // x' of the unit
   };
   const Params &p;
-  float bmax;      // max |beta * smooth|
-  double inv_n;
+  float bmax;  // max |beta * smooth|
   const uint16_t *gate_row;
   Rms post, pre;
-  __device__ __forceinline__ explicit NormsOp(const Params &q) : p(q), bmax(0.f), gate_row(nullptr) {
-    inv_n = __ddiv_rn(1.0, static_cast<double>(q.out.n));
-  }
+  __device__ __forceinline__ explicit NormsOp(const Params &q)
+      : p(q), bmax(0.f), gate_row(nullptr) {}
 
   __device__ __forceinline__ void setup(RowSmem &sm, int tid, int nt, int nwarps) {
     if (!p.beta) return;
-    unsigned b = 0u;
+    float b = 0.f;
     for (int u = tid; u < p.out.units; u += nt) {
       float2 v[4];
       unpack<T>(load_unit<VEC, false>(p.beta, u, p.out.n), v);
       times(v, p.smooth, u);
-      b = max(b, abs_bits8(v));
+      b = abs_top8(v, b);
     }
     bmax = block_max(b, sm.top, nwarps);
     __syncthreads();  // the slots are used again at once
@@ -91,116 +127,101 @@ struct NormsOp {
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = __fmul2_rn(v[k], s[k]);
   }
-
-  __device__ __forceinline__ Raw fetch(int64_t row, int u) const {
-    const int64_t off = row * p.out.n;
-    Raw w;
-    w.h = load_unit<VEC, UPT != 0>(p.h + off, u, p.out.n);
-    w.x = load_unit<VEC, UPT != 0>(p.x + off, u, p.out.n);
-    return w;
+  __device__ __forceinline__ void stage(int64_t row, int u, uint4 *slot, int stride) const {
+    const int64_t off = row * p.out.n + 8 * u;
+    copy16_async(slot, p.h + off);
+    copy16_async(slot + stride, p.x + off);
+  }
+  __device__ __forceinline__ uint4 get_h(int64_t row, int u, const uint4 *slot) const {
+    return STAGED ? slot[0] : load_unit<VEC, false>(p.h + row * p.out.n, u, p.out.n);
+  }
+  __device__ __forceinline__ uint4 get_x(int64_t row, int u, const uint4 *slot, int stride) const {
+    return STAGED ? slot[stride] : load_unit<VEC, false>(p.x + row * p.out.n, u, p.out.n);
   }
   // long rows: x' of a unit after the row's first phases, read back or made again
-  __device__ __forceinline__ Raw refetch(int64_t row, int u) const {
-    Raw w;
-    if (p.x_out) {
-      w.x = load_unit<VEC, false>(p.x_out + row * p.out.n, u, p.out.n);
-    } else {
-      w = fetch(row, u);
-      w.x = make_x(row, w, u);
-    }
-    return w;
+  __device__ __forceinline__ uint4 x_again(int64_t row, int u) const {
+    if (p.x_out) return load_unit<VEC, false>(p.x_out + row * p.out.n, u, p.out.n);
+    return make_x(row, u, get_h(row, u, nullptr), get_x(row, u, nullptr, 0));
   }
 
-  // x' of one element in fp64, from the inputs in memory
-  __device__ __forceinline__ uint16_t x64(int64_t row, int c) const {
-    const int64_t at = row * p.out.n + c;
-    double t = __dmul_rn(__dmul_rn(static_cast<double>(Cvt<T>::f1(p.h[at])), post.inv64),
-                         static_cast<double>(Cvt<T>::f1(p.gamma_post[c])));
-    if (gate_row) t = __dmul_rn(t, static_cast<double>(Cvt<T>::f1(gate_row[c])));
-    return round16<T>(__dadd_rn(static_cast<double>(Cvt<T>::f1(p.x[at])), t));
-  }
-  __device__ __forceinline__ uint4 make_x(int64_t row, const Raw &w, int u) const {
+  __device__ __forceinline__ uint4 make_x(int64_t row, int u, const uint4 &hw, const uint4 &xw) const {
     float2 h[4], x[4], G[4];
-    unpack<T>(w.h, h);
-    unpack<T>(w.x, x);
+    unpack<T>(hw, h);
+    unpack<T>(xw, x);
     unpack<T>(load_unit<VEC, false>(p.gamma_post, u, p.out.n), G);
     times(G, gate_row, u);
     const float2 f = make_float2(post.inv, post.inv);
-    const float fe = fabsf(post.inv) * 2.384185791015625e-7f;  // 2^-22
-    // products below the normal range lose up to 2^-149 each; a cold row has
-    // no binary32 bound: everything in fp64
-    const float floor_e = post.cold ? __int_as_float(0x7F800000) : fabsf(post.inv) * 1.1754944e-38f;
-    uint32_t lo[4], hi[4], differ = 0u;
+    float2 v[4];
+    float tmax = 0.f, vmax = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float2 hg = __fmul2_rn(h[k], G[k]);
-      const float2 v = __ffma2_rn(hg, f, x[k]);
-      const float2 e = make_float2(
-          __fmaf_rn(fabsf(hg.x), fe, __fmaf_rn(fabsf(v.x), 1.1920928955078125e-7f, floor_e)),
-          __fmaf_rn(fabsf(hg.y), fe, __fmaf_rn(fabsf(v.y), 1.1920928955078125e-7f, floor_e)));
-      lo[k] = Cvt<T>::pack(v.x - e.x, v.y - e.y);
-      hi[k] = Cvt<T>::pack(v.x + e.x, v.y + e.y);
+      v[k] = __ffma2_rn(hg, f, x[k]);
+      tmax = abs_max3(hg.x, hg.y, tmax);
+      vmax = abs_max3(v[k].x, v[k].y, vmax);
+    }
+    // the unit's largest error bound serves its eight elements; products below
+    // the normal range lose up to 2^-149 each; a cold row has no binary32
+    // bound: everything in fp64
+    const float floor_e = post.cold ? __int_as_float(0x7F800000) : fabsf(post.inv) * 1.1754944e-38f;
+    const float e = __fmaf_rn(tmax, fabsf(post.inv) * 2.384185791015625e-7f,
+                              __fmaf_rn(vmax, 1.1920928955078125e-7f, floor_e));
+    const float2 up = make_float2(e, e), down = make_float2(-e, -e);
+    uint32_t lo[4], hi[4], differ = 0u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 a = __fadd2_rn(v[k], down), b = __fadd2_rn(v[k], up);
+      lo[k] = Cvt<T>::pack(a.x, a.y);
+      hi[k] = Cvt<T>::pack(b.x, b.y);
       differ |= lo[k] ^ hi[k];
     }
     uint4 r = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    if (differ) {
-      const uint4 d = make_uint4(lo[0] ^ hi[0], lo[1] ^ hi[1], lo[2] ^ hi[2], lo[3] ^ hi[3]);
-      const int cnt = min(8, p.out.n - 8 * u);
-      for (int j = 0; j < cnt; ++j)
-        if (get16(d, j)) set16(r, j, x64(row, 8 * u + j));
-      if (!VEC)
-        for (int j = cnt; j < 8; ++j) set16(r, j, 0);
-    }
+    if (differ)
+      r = settle_x<T>(r, make_uint4(hi[0], hi[1], hi[2], hi[3]), hw, xw, p.gamma_post + 8 * u,
+                      gate_row ? gate_row + 8 * u : nullptr, post.inv64, p.out.n - 8 * u);
     return r;
   }
 
   template <class E>
-  __device__ __forceinline__ void prepare(RowSmem &sm, int64_t row, Raw *raw, E &&each, int nwarps) {
+  __device__ __forceinline__ void prepare(RowSmem &sm, int64_t row, Keep *keep, const uint4 *slot, int nt,
+                                          E &&each, int nwarps) {
+    const int stride = UPT * nt;
     gate_row = p.gate ? p.gate + static_cast<int64_t>(static_cast<uint32_t>(row) /
                                                       static_cast<uint32_t>(p.rows_per_gate)) *
                                      p.out.n
                       : nullptr;
     // ---- Rms of h
     double ss = 0.0;
-    each([&](int u, int i) {
-      if (UPT == 0) raw[0].h = load_unit<VEC, false>(p.h + row * p.out.n, u, p.out.n);
-      ss += sumsq<T>(raw[i].h);
-    });
+    each([&](int u, int i) { ss += sumsq<T>(get_h(row, u, slot + i * nt)); });
     ss = block_sum(ss, sm.sum[0], nwarps);
     bool cold = ss_out_of_range(ss, p.eps_post);
     if (cold) {  // the same for every thread
-      ss = 0.0;
-      each([&](int u, int i) {
-        if (UPT == 0) raw[0].h = load_unit<VEC, false>(p.h + row * p.out.n, u, p.out.n);
-        ss += sumsq64<T>(raw[i].h);
-      });
+      ss = sumsq_cold<T>(p.h + row * p.out.n, nullptr, nullptr, nullptr, nullptr, 0.0, p.out.n);
       ss = block_sum(ss, sm.sum[2], nwarps);
     }
-    post = make_rms(ss, inv_n, p.eps_post, p.alpha, cold);
+    post = make_rms(ss, p.inv_n, p.eps_post, p.alpha, cold);
     // ---- x' and its Rms
     ss = 0.0;
     each([&](int u, int i) {
-      if (UPT == 0) raw[0] = fetch(row, u);
-      raw[i].x = make_x(row, raw[i], u);
-      ss += sumsq<T>(raw[i].x);
-      if (p.x_out) store_unit<VEC>(p.x_out + row * p.out.n, u, p.out.n, raw[i].x);
+      keep[i].x = make_x(row, u, get_h(row, u, slot + i * nt), get_x(row, u, slot + i * nt, stride));
+      ss += sumsq<T>(keep[i].x);
+      if (p.x_out) store_unit<VEC>(p.x_out + row * p.out.n, u, p.out.n, keep[i].x);
     });
     ss = block_sum(ss, sm.sum[1], nwarps);
     cold = ss_out_of_range(ss, p.eps);
     if (cold) {
-      ss = 0.0;
-      each([&](int u, int i) {
-        if (UPT == 0) raw[0] = refetch(row, u);
-        ss += sumsq64<T>(raw[i].x);
-      });
+      const int64_t off = row * p.out.n;  // (x' stored by other threads: a barrier has passed)
+      ss = sumsq_cold<T>(p.x_out ? p.x_out + off : nullptr, p.h + off, p.x + off, p.gamma_post, gate_row,
+                         post.inv64, p.out.n);
       ss = block_sum(ss, sm.sum[2], nwarps);
     }
-    pre = make_rms(ss, inv_n, p.eps, 1.f, cold);
+    pre = make_rms(ss, p.inv_n, p.eps, 1.f, cold);
   }
 
-  __device__ __forceinline__ void value(const Raw &w, int u, float2 v[4]) const {
+  __device__ __forceinline__ bool value(int64_t row, int u, Keep &keep, const uint4 *, int, float2 v[4]) const {
+    if (UPT == 0) keep.x = x_again(row, u);
     float2 x[4], G[4], B[4];
-    unpack<T>(w.x, x);
+    unpack<T>(keep.x, x);
     unpack<T>(load_unit<VEC, false>(p.gamma, u, p.out.n), G);
     times(G, p.smooth, u);
     const float2 r = make_float2(pre.inv, pre.inv);
@@ -213,18 +234,14 @@ struct NormsOp {
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = __fmul2_rn(__fmul2_rn(x[k], r), G[k]);
     }
-    if (pre.cold) {  // no binary32 bound: a maximum that sends the row to fp64
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float f = 8 * u + j < p.out.n ? __double2float_rn(value64(w, u, j)) : 0.f;
-        if (j & 1) v[j >> 1].y = f;
-        else v[j >> 1].x = f;
-      }
-    }
+    return !pre.cold;
   }
-  __device__ __forceinline__ double value64(const Raw &w, int u, int j) const {
-    const int c = 8 * u + j;
-    double y = __dmul_rn(__dmul_rn(static_cast<double>(Cvt<T>::f1(get16(w.x, j))), pre.inv64),
+  __device__ __forceinline__ double value64(int64_t row, int c) const {
+    const int64_t at = row * p.out.n + c;
+    const uint16_t x = p.x_out ? p.x_out[at]
+                               : x64<T>(p.h[at], p.x[at], p.gamma_post + c, gate_row ? gate_row + c : nullptr,
+                                        post.inv64);
+    double y = __dmul_rn(__dmul_rn(static_cast<double>(Cvt<T>::f1(x)), pre.inv64),
                          static_cast<double>(Cvt<T>::f1(p.gamma[c])));
     if (p.beta) y = __dadd_rn(y, static_cast<double>(Cvt<T>::f1(p.beta[c])));
     if (p.smooth) y = __dmul_rn(y, static_cast<double>(Cvt<T>::f1(p.smooth[c])));
@@ -235,7 +252,7 @@ struct NormsOp {
     return __fmaf_rn(2.f, bmax, M) * 4.76837158203125e-7f;
   }
   // (Q + 2 bmax / scale) 2^-20: the same over the scale, and its reciprocal's error
-  __device__ __forceinline__ float tolerance(const Raw &, int, float, float inv) const {
+  __device__ __forceinline__ float coarse(const Keep &, float inv) const {
     return __fmaf_rn(2.f * bmax, inv, QT == 1 ? 7.f : 127.f) * 9.5367431640625e-7f;
   }
 };

@@ -7,11 +7,15 @@
 // finds the row maximum, the scale RN32(max|in| / Q) and the codes
 // RNE(in / scale) that the fp64 values give:
 //   - the binary32 maximum M is within the error bound of the true one, so
-//     the true maximum is among the elements whose binary32 value comes that
-//     close to M: their fp64 values are reduced (an integer maximum of their
-//     bit patterns, the same in any order), usually one element a row;
+//     the true maximum is in a unit whose binary32 values come that close to
+//     M: the fp64 values of those units are reduced (an integer maximum of
+//     their bit patterns, the same in any order), usually one unit a row;
 //   - a code is decided in binary32 unless the quotient lies within its error
-//     of a half-way point; then by the fp64 value (code_exact).
+//     of a half-way point; the codes of units with such a one are decided by
+//     their fp64 values (code_exact).
+// The fp64 work is done by warps together, eight lanes to a unit, in code kept
+// out of the row's main path, which has to stay in the instruction cache (in
+// line in every unit it cost 217 us instead of 150 on the norms of 8192 x 4096).
 // Rows whose maximum is below kTiny, above kHuge or not finite are computed
 // in fp64 throughout.  A row holding a NaN gets scale NaN, one holding an
 // infinity scale infinity (NaN if both), both with codes 0; an all-zero row
@@ -26,7 +30,7 @@
 
 namespace arnq {
 
-constexpr float kTiny = 1e-25f, kHuge = 1e37f;
+constexpr float kTiny = 1e-18f, kHuge = 1e37f;
 constexpr int kQNone = 2;  // no codes: the values themselves in 16 bits
 
 // ------------------------------------------------------------ units of eight
@@ -108,16 +112,6 @@ __device__ __forceinline__ double sumsq(const uint4 &w) {
   }
   return s;
 }
-template <class T>
-__device__ __forceinline__ double sumsq64(const uint4 &w) {
-  double s = 0.0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const double v = static_cast<double>(Cvt<T>::f1(get16(w, j)));
-    s = __fma_rn(v, v, s);
-  }
-  return s;
-}
 
 // ------------------------------------------------------------ block reductions
 
@@ -129,12 +123,18 @@ struct RowSmem {
   unsigned long long cand[2];  // fp64 maxima of a row, by row parity
 };
 
-// Sum over the CTA (every warp takes part); one barrier.
+// Sum over the CTA (every warp takes part); one barrier, none for one warp.
 __device__ __forceinline__ double block_sum(double v, double *slots, int nwarps) {
   v = warp_sum_d(v);
-  if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
-  __syncthreads();
+  if (nwarps == 1) return v;
   const int lane = threadIdx.x & 31;
+  if (lane == 0) slots[threadIdx.x >> 5] = v;
+  __syncthreads();
+  if (nwarps <= 4) {
+    double s = slots[0] + slots[1];
+    for (int i = 2; i < nwarps; ++i) s += slots[i];
+    return s;
+  }
   double s = lane < nwarps ? slots[lane] : 0.0;
   for (int o = 16; o > 0; o >>= 1)
     if (o < nwarps) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
@@ -142,13 +142,17 @@ __device__ __forceinline__ double block_sum(double v, double *slots, int nwarps)
 }
 // Maximum of non-negative floats over the CTA by their bit patterns, which
 // put a NaN above everything; one barrier.
-__device__ __forceinline__ float block_max(unsigned bits, unsigned *slots, int nwarps) {
-  bits = __reduce_max_sync(0xFFFFFFFFu, bits);
-  if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = bits;
-  __syncthreads();
+__device__ __forceinline__ float block_max(float v, unsigned *slots, int nwarps) {
+  const unsigned bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v));
   const int lane = threadIdx.x & 31;
+  if (lane == 0) slots[threadIdx.x >> 5] = bits;
+  __syncthreads();
   return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, lane < nwarps ? slots[lane] : 0u));
 }
+
+// IEEE division and square root, out of line: used by rare rows
+static __device__ __noinline__ double div_ieee(double a, double b) { return __ddiv_rn(a, b); }
+static __device__ __noinline__ double sqrt_ieee(double a) { return __dsqrt_rn(a); }
 
 // m / Q rounded once to fp64, for Q = 127 or 7: a quotient from the rounded
 // reciprocal, corrected by its exact remainder (Markstein's theorem: the
@@ -160,20 +164,28 @@ __device__ __forceinline__ double div_q(double m) {
   return __fma_rn(__fma_rn(-static_cast<double>(Q), q, m), r, q);
 }
 
+// max(|a|, |b|, |c|) in one instruction; abs_max3 ignores NaN, abs_max3_nan
+// returns it
+__device__ __forceinline__ float abs_max3(float a, float b, float c) {
+  float d;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float abs_max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ float abs_max8(const float2 v[4]) {
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
+  for (int i = 0; i < 4; ++i) m = abs_max3(v[i].x, v[i].y, m);
   return m;
 }
-// the largest bit pattern of |v|: NaN counts as the largest
-__device__ __forceinline__ unsigned abs_bits8(const float2 v[4]) {
-  unsigned m = 0u;
+// |v|'s largest bit pattern, NaN counting as the largest, with `m` so far
+__device__ __forceinline__ float abs_top8(const float2 v[4], float m) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    m = max(m, __float_as_uint(v[i].x) & 0x7FFFFFFFu);
-    m = max(m, __float_as_uint(v[i].y) & 0x7FFFFFFFu);
-  }
+  for (int i = 0; i < 4; ++i) m = abs_max3_nan(v[i].x, v[i].y, m);
   return m;
 }
 __device__ __forceinline__ float elem(const float2 v[4], int j) {
@@ -189,24 +201,61 @@ struct RowOut {
   int32_t units;  // ceil(n / 8)
 };
 
+// ------------------------------------------------------------ staging
+
+// The next row's inputs wait in shared memory, copied by each thread for
+// itself (16 bytes at a time, asynchronously): slot (tensor, i) of thread tid
+// holds unit tid + i*nt of that tensor.  A thread reads only what it copied,
+// so its own wait is all the synchronisation there is.
+__device__ __forceinline__ void copy16_async(uint4 *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
 // ------------------------------------------------------------ the kernel
 
+// The fp64 values of the units flagged by the lanes of a warp: eight lanes a
+// unit, four units a round.  flags: bit i for the lane's unit first + i*step;
+// use(u, c, in): in = value64(row, c) of column c = 8u + lane % 8 (0 behind the
+// row's end), called by every lane; u < 0 for lanes without a unit.
+template <int NU, class Op, class Use>
+__device__ __forceinline__ void flagged_units(const Op &op, int64_t row, unsigned flags, int first, int step,
+                                              int n, Use &&use) {
+  const int lane = threadIdx.x & 31, group = lane >> 3;
+#pragma unroll 1
+  for (int i = 0; i < NU; ++i) {
+    unsigned who = __ballot_sync(0xFFFFFFFFu, (flags >> i) & 1u);
+    while (who) {
+      unsigned mine = who;
+      for (int g = 0; g < group; ++g) mine &= mine - 1u;
+      for (int g = 0; g < 4; ++g) who &= who - 1u;
+      const int u = mine ? first - lane + (__ffs(mine) - 1) + i * step : -1;
+      const int c = 8 * u + (lane & 7);
+      use(u, c, u >= 0 && c < n ? op.value64(row, c) : 0.0);
+    }
+  }
+}
+
 // Op: struct with
-//   Params, T, VEC, UPT (units per thread held in registers; 0: rows longer
-//   than that are read again in every phase), QT (ARNQ code type 0 INT8,
-//   1 INT4, kQNone)
-//   Raw, fetch(row, u) -> Raw       a unit's inputs
-//   begin(row), prepare(...)        the row's statistics
-//   value(raw, u, v)                a unit's binary32 values
-//   value64(raw, u, j)              one value in fp64
+//   Params, T, VEC (16-byte units), UPT (units per thread held in registers;
+//   0: rows longer than that are read again in every phase), QT (code type:
+//   0 INT8, 1 INT4, kQNone), STAGED (inputs staged as above), kInputs
+//   (tensors staged), Keep (what a unit keeps besides its values)
+//   stage(row, u, slot, stride)     issues the copies of a unit
+//   prepare(...)                    the row's statistics
+//   value(row, u, keep, ..., v)     a unit's binary32 values; returns false
+//                                   where they have no error bound
+//   value64(row, c)                 one value in fp64, from memory
 //   slack(M)                        bound on |value - value64| over the row
-//   tolerance(raw, j, t, inv)       bound on the error of the quotient t
+//   coarse(keep, inv)               bound on the error of a unit's quotients
 template <class Op>
-__global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel(typename Op::Params p) {
+__global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel(const __grid_constant__ typename Op::Params p) {
   constexpr int UPT = Op::UPT, NU = UPT > 0 ? UPT : 1;
   constexpr bool VEC = Op::VEC;
   constexpr int Q = Op::QT == 1 ? 7 : 127;
   __shared__ RowSmem sm;
+  extern __shared__ uint4 slots[];
   const int tid = threadIdx.x, nt = blockDim.x, nwarps = nt >> 5;
   const RowOut &out = p.out;
   const int n = out.n, units = out.units;
@@ -216,10 +265,6 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   Op op(p);
-  op.setup(sm, tid, nt, nwarps);
-  if (tid < 2) sm.cand[tid] = 0ull;
-
-  typename Op::Raw raw[NU], next[NU];
   auto each = [&](auto &&f) {
     if (UPT > 0) {
 #pragma unroll
@@ -231,124 +276,154 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
       for (int u = tid; u < units; u += nt) f(u, 0);
     }
   };
+  // f(u, i) sets the lane's flag of a unit; then the flagged units in fp64
+  auto each_flagged = [&](int64_t row, auto &&f, auto &&use) {
+    if (UPT > 0) {
+      unsigned flags = 0u;
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        const int u = tid + i * nt;
+        if (u < units && f(u, i)) flags |= 1u << i;
+      }
+      __syncwarp();
+      if (__any_sync(0xFFFFFFFFu, flags != 0u)) flagged_units<NU>(op, row, flags, tid, nt, n, use);
+    } else {
+      for (int u0 = tid & ~31; u0 < units; u0 += nt) {  // whole warps
+        const int u = u0 + (tid & 31);
+        const unsigned flags = u < units && f(u, 0) ? 1u : 0u;
+        __syncwarp();
+        flagged_units<1>(op, row, flags, u, 0, n, use);
+      }
+    }
+  };
   int64_t row = blockIdx.x;
-  if (UPT > 0 && row < out.rows) each([&](int u, int i) { next[i] = op.fetch(row, u); });
+  auto stage = [&](int64_t r) {
+    if (Op::STAGED) {
+      if (r < out.rows)
+        each([&](int u, int i) { op.stage(r, u, slots + i * nt + tid, UPT * nt); });
+      copies_commit();
+    }
+  };
+  stage(row);
+  op.setup(sm, tid, nt, nwarps);
+  if (tid < 2) sm.cand[tid] = 0ull;
 
   int parity = 0;
   for (; row < out.rows; row += gridDim.x, parity ^= 1) {
-    if (UPT > 0) {
-#pragma unroll
-      for (int i = 0; i < NU; ++i) raw[i] = next[i];
-      const int64_t nr = row + gridDim.x;
-      if (nr < out.rows) each([&](int u, int i) { next[i] = op.fetch(nr, u); });
-    }
-    op.prepare(sm, row, raw, each, nwarps);
+    typename Op::Keep keep[NU];
     float2 v[NU][4];
-    auto take = [&](int u, int i) {  // long rows: a unit's values, made again
-      if (UPT == 0) {
-        raw[0] = op.refetch(row, u);
-        op.value(raw[0], u, v[0]);
-      }
-    };
+    if (Op::STAGED) copies_wait();
+    op.prepare(sm, row, keep, slots + tid, nt, each, nwarps);
 
     if (Op::QT == kQNone) {
+      if (Op::STAGED) stage(row + gridDim.x);  // prepare() has read the slots, behind a barrier
       uint16_t *yr = reinterpret_cast<uint16_t *>(out.y) + row * n;
-      each([&](int u, int i) {
-        if (UPT > 0) op.value(raw[i], u, v[i]);
-        take(u, i);
-        uint32_t w[4];
+      each_flagged(
+          row,
+          [&](int u, int i) {
+            const bool ok = op.value(row, u, keep[i], slots + i * nt + tid, UPT * nt, v[i]);
+            uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = Cvt<typename Op::T>::pack(v[i][k].x, v[i][k].y);
-        store_unit<VEC>(yr, u, n, make_uint4(w[0], w[1], w[2], w[3]));
-      });
+            for (int k = 0; k < 4; ++k) w[k] = Cvt<typename Op::T>::pack(v[i][k].x, v[i][k].y);
+            store_unit<VEC>(yr, u, n, make_uint4(w[0], w[1], w[2], w[3]));
+            return !ok;
+          },
+          [&](int u, int c, double in) {
+            if (u >= 0 && c < n) yr[c] = round16<typename Op::T>(in);
+          });
       continue;
     }
 
     // ---- row maximum in binary32
-    unsigned bits = 0u;
+    float top32 = 0.f;
     each([&](int u, int i) {
-      if (UPT > 0) op.value(raw[i], u, v[i]);
-      take(u, i);
-      bits = max(bits, abs_bits8(v[i]));
+      if (!op.value(row, u, keep[i], slots + i * nt + tid, UPT * nt, v[i])) top32 = __int_as_float(0x7F800000);
+      top32 = abs_top8(v[i], top32);
     });
-    const float M = block_max(bits, sm.top, nwarps);
+    const float M = block_max(top32, sm.top, nwarps);
+    stage(row + gridDim.x);  // the values of this row's slots have met the barrier
     const bool wide = !(M >= kTiny && M <= kHuge);  // the whole row in fp64
     if (tid == 0) sm.cand[parity ^ 1] = 0ull;       // the next row's
 
-    // ---- fp64 maximum over the elements that may hold it
+    // ---- fp64 maximum over the units that may hold it
     const float thr = M - 2.f * op.slack(M);
-    each([&](int u, int i) {
-      if (UPT == 0) take(u, i);
-      if (!wide && abs_max8(v[i]) < thr) return;
-      const int cnt = min(8, n - 8 * u);
-      for (int j = 0; j < cnt; ++j) {
-        float a = 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) a = j == k ? fabsf(elem(v[i], k)) : a;
-        if (!wide && a < thr) continue;
-        atomicMax(&sm.cand[parity], static_cast<unsigned long long>(
-                                        __double_as_longlong(fabs(op.value64(raw[i], u, j)))));
-      }
-    });
+    if (__any_sync(0xFFFFFFFFu, wide || top32 >= thr)) {
+      unsigned long long best = 0ull;
+      each_flagged(
+          row,
+          [&](int u, int i) {
+            if (UPT == 0) op.value(row, u, keep[i], slots, 0, v[i]);
+            return wide || abs_max8(v[i]) >= thr;
+          },
+          [&](int, int, double in) {
+            best = max(best, static_cast<unsigned long long>(__double_as_longlong(fabs(in))));
+          });
+      if (best) atomicMax(&sm.cand[parity], best);
+    }
     __syncthreads();
     const double top = __longlong_as_double(static_cast<long long>(sm.cand[parity]));
-    const double dq = wide ? __ddiv_rn(top, static_cast<double>(Q)) : div_q<Q>(top);
-    const float sc = __double2float_rn(dq);
+    const float sc = __double2float_rn(wide ? div_ieee(top, static_cast<double>(Q)) : div_q<Q>(top));
     if (tid == 0) out.scale[row] = sc;
     const bool finite = sc > 0.f && sc <= 3.402823466e38f;  // else every code is 0
-    const float inv = __frcp_rn(sc);
+    const float inv = __fdividef(1.f, sc);
 
     // ---- codes
     const int64_t code_bytes = Op::QT == 1 ? n / 2 : n;
     uint8_t *yr = out.y + row * code_bytes;
-    each([&](int u, int i) {
-      if (UPT == 0) take(u, i);
-      uint32_t q[8];
-      unsigned near = 0u;
+    each_flagged(
+        row,
+        [&](int u, int i) {
+          if (UPT == 0) op.value(row, u, keep[i], slots, 0, v[i]);
+          // t = value/scale; adding kMagic rounds it to a whole number whose
+          // low bits are the code; what was rounded off tells how near a
+          // half-way point it was
+          uint32_t q[8];
+          float off = 0.f;
+          const float2 inv2 = make_float2(inv, inv), mag = make_float2(kMagic, kMagic),
+                       neg = make_float2(-kMagic, -kMagic), minus = make_float2(-1.f, -1.f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float t = elem(v[i], j) * inv;
-        const float r = t + kMagic;
-        q[j] = __float_as_uint(r);
-        const float d = t - (r - kMagic);
-        if (fabsf(fabsf(d) - 0.5f) <= op.tolerance(raw[i], j, t, inv)) near |= 1u << j;
-      }
-      if (wide) near = finite ? 0xFFu : 0u;
-      const int cnt = min(8, n - 8 * u);
-      if (!VEC) near &= (1u << cnt) - 1u;
-      // bytes (INT8) or nibbles (INT4) of the eight codes, column 0 lowest
-      uint64_t w = 0;
-      if (Op::QT == 0) {
-        const uint32_t lo = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
-        const uint32_t hi = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
-        w = static_cast<uint64_t>(hi) << 32 | lo;
-      } else {
-        uint32_t x = 0;
+          for (int k = 0; k < 4; ++k) {
+            const float2 t = __fmul2_rn(v[i][k], inv2);
+            const float2 r = __fadd2_rn(t, mag);
+            const float2 d = __ffma2_rn(__fadd2_rn(r, neg), minus, t);
+            off = abs_max3(d.x, d.y, off);
+            q[2 * k] = __float_as_uint(r.x);
+            q[2 * k + 1] = __float_as_uint(r.y);
+          }
+          uint32_t lo, hi;  // eight codes, column 0 lowest
+          if (Op::QT == 0) {
+            lo = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+            hi = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
+          } else {
+            const uint32_t even = __byte_perm(__byte_perm(q[0], q[2], 0x0040), __byte_perm(q[4], q[6], 0x0040), 0x5410);
+            const uint32_t odd = __byte_perm(__byte_perm(q[1], q[3], 0x0040), __byte_perm(q[5], q[7], 0x0040), 0x5410);
+            lo = (even & 0x0F0F0F0Fu) | ((odd << 4) & 0xF0F0F0F0u);
+            hi = 0u;
+          }
+          if (VEC) {
+            if (Op::QT == 0) reinterpret_cast<uint2 *>(yr)[u] = make_uint2(lo, hi);
+            else reinterpret_cast<uint32_t *>(yr)[u] = lo;
+          } else {
+            const int cnt = min(8, n - 8 * u), bytes = Op::QT == 0 ? cnt : cnt / 2;
+            uint8_t *to = yr + static_cast<int64_t>(u) * (Op::QT == 0 ? 8 : 4);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x |= (q[j] & 0xFu) << (4 * j);
-        w = x;
-      }
-      if (wide) w = 0;
-      while (near) {
-        const int j = __ffs(near) - 1;
-        near &= near - 1u;
-        const double in = op.value64(raw[i], u, j);
-        int code;
-        if (wide) code = in == in ? code_of(in, sc, Q) : 0;
-        else code = code_exact(in, sc, __double2float_rn(in) * inv, Q);
-        const int width = Op::QT == 1 ? 4 : 8;
-        const uint64_t mask = ((1ull << width) - 1ull) << (width * j);
-        w = (w & ~mask) | ((static_cast<uint64_t>(static_cast<uint32_t>(code)) << (width * j)) & mask);
-      }
-      if (VEC) {
-        if (Op::QT == 0) reinterpret_cast<uint2 *>(yr)[u] = make_uint2(static_cast<uint32_t>(w), static_cast<uint32_t>(w >> 32));
-        else reinterpret_cast<uint32_t *>(yr)[u] = static_cast<uint32_t>(w);
-      } else if (Op::QT == 0) {
-        for (int j = 0; j < cnt; ++j) yr[8 * u + j] = static_cast<uint8_t>(w >> (8 * j));
-      } else {
-        for (int j = 0; j < cnt / 2; ++j) yr[4 * u + j] = static_cast<uint8_t>(w >> (8 * j));
-      }
-    });
+            for (int j = 0; j < (Op::QT == 0 ? 8 : 4); ++j)
+              if (j < bytes) to[j] = static_cast<uint8_t>((j < 4 ? lo : hi) >> (8 * (j & 3)));
+          }
+          return wide || off >= 0.5f - op.coarse(keep[i], inv);
+        },
+        [&](int u, int c, double in) {
+          int code = 0;
+          if (finite && in == in)
+            code = wide ? code_of_t(div_ieee(in, static_cast<double>(sc)), Q)
+                        : code_exact(in, sc, __double2float_rn(in) * inv, Q);
+          if (Op::QT == 0) {
+            if (u >= 0 && c < n) yr[c] = static_cast<uint8_t>(code);
+          } else {
+            const int up = __shfl_down_sync(0xFFFFFFFFu, code, 1);
+            if (u >= 0 && c < n && (c & 1) == 0) yr[c >> 1] = static_cast<uint8_t>((code & 0xF) | (up << 4));
+          }
+        });
   }
   // the next kernel on the stream may start its set-up (it waits for this
   // grid's completion before touching memory)

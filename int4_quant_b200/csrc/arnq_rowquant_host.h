@@ -29,9 +29,12 @@ inline int kernel_qt(int qdt) {
 }
 
 // Units of eight per thread (0: the row is read again in every phase) and
-// threads for a row of `units`.
-inline void row_threads(int units, int *upt, int *threads) {
-  if (units <= 1024) *upt = 1;
+// threads for a row of `units`.  Four units a thread where rows outnumber the
+// SMs and max4 such threads hold the row (a row's fixed cost, reductions and barriers, is then shared by few
+// threads); with fewer rows the row's latency counts: the most threads.
+inline void row_threads(int units, bool many, int max4, int *upt, int *threads) {
+  if (many && units <= 4 * max4) *upt = units <= 32 ? 1 : 4;
+  else if (units <= 1024) *upt = 1;
   else if (units <= 2048) *upt = 2;
   else *upt = 0;
   const int per = *upt == 0 ? 2 : *upt;
@@ -46,11 +49,12 @@ arnq_status launch_rows(typename Op::Params p, int threads, cudaStream_t stream)
   int dev = 0, sms = 0, per_sm = 0;
   arnq_status st = current_device(&dev, &sms);
   if (st != ARNQ_OK) return st;
-  st = resident_ctas(fn, dev, threads, 0, &per_sm);
+  const int smem = Op::STAGED ? Op::kInputs * Op::UPT * threads * 16 : 0;
+  st = resident_ctas(fn, dev, threads, smem, &per_sm);
   if (st != ARNQ_OK) return st;
   const int64_t slots = static_cast<int64_t>(per_sm) * sms;
   return launch_dependent(fn, dim3(static_cast<unsigned>(p.out.rows < slots ? p.out.rows : slots)),
-                          threads, 0, 1, stream, &p);
+                          threads, smem, 1, stream, &p);
 }
 
 }  // namespace arnq
