@@ -31,16 +31,41 @@ struct GluParams {
   const uint16_t *smooth;  // [n] or nullptr
 };
 
-// one value in fp64: g[0], u = g[n]
+// 1 / (1 + exp(-z)) in fp64 to some 1e-14, for decisions that sit many orders
+// of magnitude above that: exp(-z) = 2^k exp(r), |r| <= ln2 / 2 (ln2 taken
+// off in two parts, the first of 32 bits so that k times it is exact: Cody and
+// Waite's reduction), by its Taylor
+// series to r^12 (the next term is below 2e-16), paired up to shorten the
+// chain (Estrin's scheme); the reciprocal from the binary32 one by Newton
+// steps.  Beyond +-700 the sigmoid is 1 or too small for any output.
+__device__ __forceinline__ double sigmoid64(double z) {
+  const double y = fmin(fmax(-z, -700.0), 700.0);
+  const double kf = rint(y * 1.4426950408889634);
+  const double r = __fma_rn(kf, -1.9082149292705877e-10, __fma_rn(kf, -0.6931471803691238, y));
+  const double r2 = r * r, r4 = r2 * r2;
+  const double a0 = 1.0 + r, a1 = __fma_rn(r, 1.0 / 6, 0.5), a2 = __fma_rn(r, 1.0 / 120, 1.0 / 24),
+               a3 = __fma_rn(r, 1.0 / 5040, 1.0 / 720), a4 = __fma_rn(r, 1.0 / 362880, 1.0 / 40320),
+               a5 = __fma_rn(r, 1.0 / 39916800, 1.0 / 3628800);
+  const double b0 = __fma_rn(r2, a1, a0), b1 = __fma_rn(r2, a3, a2),
+               b2 = __fma_rn(r2, __fma_rn(r2, 1.0 / 479001600, a5), a4);
+  const double e = __fma_rn(r4, __fma_rn(r4, b2, b1), b0);
+  const double d = 1.0 + e * __longlong_as_double(static_cast<long long>(static_cast<int>(kf) + 1023) << 52);
+  if (d > 1e37) return div_ieee(1.0, d);
+  double q = static_cast<double>(__fdividef(1.f, __double2float_rn(d)));
+  q = __fma_rn(__fma_rn(-d, q, 1.0), q, q);
+  return __fma_rn(__fma_rn(-d, q, 1.0), q, q);
+}
+// one value in fp64 (a gate of minus infinity: infinity times zero)
 template <class T, int ACT>
-__device__ __noinline__ double glu64(const uint16_t *gate, int n, const uint16_t *smooth) {
-  const double g = static_cast<double>(Cvt<T>::f1(gate[0]));
-  const double t = static_cast<double>(Cvt<T>::f1(gate[n]));
+__device__ __noinline__ double glu64(const uint16_t *gate, const uint16_t *up, const uint16_t *smooth) {
+  const double g = static_cast<double>(Cvt<T>::f1(*gate));
+  const double t = static_cast<double>(Cvt<T>::f1(*up));
   if (g == 0.0 || t == 0.0) return __dmul_rn(g, t);  // (0 times an infinity or NaN is NaN)
+  if (g < -1e300) return __longlong_as_double(0x7FF8000000000000ll);
   double z = g;
   if (ACT == ACT_GELU_TANH) z = 1.5957691216057308 * (g + 0.044715 * g * g * g);
-  const double in = g / (1.0 + exp(-z)) * t;
-  return smooth ? in * static_cast<double>(Cvt<T>::f1(smooth[0])) : in;
+  const double in = g * sigmoid64(z) * t;
+  return smooth ? in * static_cast<double>(Cvt<T>::f1(*smooth)) : in;
 }
 
 template <class T_, int ACT, int QT_, bool VEC_, int UPT_>
@@ -48,6 +73,7 @@ struct GluOp {
   typedef T_ T;
   typedef GluParams Params;
   static constexpr int QT = QT_, UPT = UPT_, kInputs = 2;
+  static constexpr bool kReadsSlots = true;
   static constexpr bool VEC = VEC_, STAGED = VEC_ && UPT_ > 0;
   static constexpr int kMaxThreads = UPT == 4 ? 512 : 1024, kMinCtas = UPT == 4 ? 2 : 1;
   struct Keep {
@@ -106,7 +132,7 @@ struct GluOp {
     for (int k = 0; k < 4; ++k) {
       // g * sigmoid(z) * u * smooth, exp(-z) = 2^(-z log2 e)
       const float2 z = arg2(g[k]);
-      low = fminf(low, fminf(z.x, z.y));
+      asm("min.f32 %0, %1, %2, %3;" : "=f"(low) : "f"(z.x), "f"(z.y), "f"(low));
       const float2 y = __fmul2_rn(z, l);
       const float2 e = __fadd2_rn(make_float2(exp2_approx(y.x), exp2_approx(y.y)), one);
       v[k] = __fmul2_rn(__fmul2_rn(g[k], make_float2(rcp_approx(e.x), rcp_approx(e.y))), t[k]);
@@ -116,8 +142,13 @@ struct GluOp {
     // huge factor
     return !(low < kLow) || abs_max8(t) <= 1e8f;
   }
-  __device__ __forceinline__ double value64(int64_t row, int c) const {
-    return glu64<T, ACT>(gate_of(row) + c, p.out.n, p.smooth ? p.smooth + c : nullptr);
+  __device__ __forceinline__ double value64(int64_t row, int c, const uint4 *at) const {
+    const uint16_t *g = gate_of(row) + c, *t = g + p.out.n;
+    if (at) {
+      g = reinterpret_cast<const uint16_t *>(at) + c;
+      t = g + 8 * UPT * static_cast<int>(blockDim.x);
+    }
+    return glu64<T, ACT>(g, t, p.smooth ? p.smooth + c : nullptr);
   }
   // candidates for the maximum: 2^-13 covers the error for every z >= kLow
   __device__ __forceinline__ float slack(float M) const { return M * 1.220703125e-4f; }

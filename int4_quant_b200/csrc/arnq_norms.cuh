@@ -7,10 +7,10 @@
 //   scale = row_max(|in|) / Q, code = round(in / scale); or RN16(in), no codes
 //
 // x' is decided like the codes: the binary32 sum v = x + h*G*(alpha/Rms(h)),
-// G = gamma_post*gate (exact: two 16-bit values), carries an error e of at
-// most |h*G*alpha/Rms| 2^-22 + |v| 2^-23 (two roundings of the factor, one of
-// the fused multiply-add, with a margin of two); where v - e and v + e round
-// to different 16-bit values the element is recomputed in fp64.
+// G = gamma_post*gate (exact: two 16-bit values), carries an error of a few
+// 2^-24 of its terms (kFactorError, kSumError below); where both ends of that
+// interval do not round to the same 16-bit value the element is recomputed in
+// fp64 (1e-4 of the elements in bf16, 1e-3 in fp16).
 #pragma once
 
 #include "arnq_rowquant.cuh"
@@ -68,9 +68,15 @@ __device__ __forceinline__ uint16_t x64(uint16_t h, uint16_t x, const uint16_t *
 template <class T>
 __device__ __noinline__ uint4 settle_x(uint4 lo, uint4 hi, uint4 h, uint4 x, const uint16_t *gamma_post,
                                        const uint16_t *gate, double inv, int count) {
+  unsigned m = 0u;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t d = word_of(lo, k) ^ word_of(hi, k);
+    m |= (d & 0xFFFFu ? 1u << (2 * k) : 0u) | (d >> 16 ? 2u << (2 * k) : 0u);
+  }
 #pragma unroll 1
-  for (int j = 0; j < 8; ++j) {
-    if (get16(lo, j) == get16(hi, j)) continue;
+  for (; m; m &= m - 1u) {
+    const int j = __ffs(m) - 1;
     set16(lo, j, j < count ? x64<T>(get16(h, j), get16(x, j), gamma_post + j, gate ? gate + j : nullptr, inv)
                            : static_cast<uint16_t>(0));
   }
@@ -96,11 +102,17 @@ struct NormsOp {
   typedef T_ T;
   typedef NormsParams Params;
   static constexpr int QT = QT_, UPT = UPT_, kInputs = 2;
+  static constexpr bool kReadsSlots = false;  // after prepare()
   static constexpr bool VEC = VEC_, STAGED = VEC_ && UPT_ > 0;
   static constexpr int kMaxThreads = UPT == 4 ? 384 : 1024, kMinCtas = UPT == 4 ? 2 : 1;
   struct Keep {
     uint4 x;  // x' of the unit
   };
+  // Error of v = x + (h G) f in units of 2^-24: the factor f one of |h G f|, the
+  // product h G none in bf16 (8 + 16 bits) and one in fp16 (11 + 22), the
+  // fused multiply-add one of |v|; and the bound's own roundings (v +- e).
+  static constexpr float kFactorError = (Cvt<T>::kBits == 8 ? 1.25f : 2.25f) * 5.9604644775390625e-8f;
+  static constexpr float kSumError = 2.25f * 5.9604644775390625e-8f;
   const Params &p;
   float bmax;  // max |beta * smooth|
   const uint16_t *gate_row;
@@ -152,27 +164,24 @@ struct NormsOp {
     times(G, gate_row, u);
     const float2 f = make_float2(post.inv, post.inv);
     float2 v[4];
-    float tmax = 0.f, vmax = 0.f;
+    float tmax = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float2 hg = __fmul2_rn(h[k], G[k]);
       v[k] = __ffma2_rn(hg, f, x[k]);
       tmax = abs_max3(hg.x, hg.y, tmax);
-      vmax = abs_max3(v[k].x, v[k].y, vmax);
     }
-    // the unit's largest error bound serves its eight elements; products below
-    // the normal range lose up to 2^-149 each; a cold row has no binary32
-    // bound: everything in fp64
+    // the unit's largest |h G| serves its eight elements; products below the
+    // normal range lose up to 2^-149 each; a cold row has no binary32 bound:
+    // everything in fp64
     const float floor_e = post.cold ? __int_as_float(0x7F800000) : fabsf(post.inv) * 1.1754944e-38f;
-    const float e = __fmaf_rn(tmax, fabsf(post.inv) * 2.384185791015625e-7f,
-                              __fmaf_rn(vmax, 1.1920928955078125e-7f, floor_e));
-    const float2 up = make_float2(e, e), down = make_float2(-e, -e);
+    const float e = __fmaf_rn(tmax, fabsf(post.inv) * kFactorError, floor_e);
     uint32_t lo[4], hi[4], differ = 0u;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float2 a = __fadd2_rn(v[k], down), b = __fadd2_rn(v[k], up);
-      lo[k] = Cvt<T>::pack(a.x, a.y);
-      hi[k] = Cvt<T>::pack(b.x, b.y);
+      const float ex = __fmaf_rn(fabsf(v[k].x), kSumError, e), ey = __fmaf_rn(fabsf(v[k].y), kSumError, e);
+      lo[k] = Cvt<T>::pack(v[k].x - ex, v[k].y - ey);
+      hi[k] = Cvt<T>::pack(v[k].x + ex, v[k].y + ey);
       differ |= lo[k] ^ hi[k];
     }
     uint4 r = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -236,7 +245,7 @@ struct NormsOp {
     }
     return !pre.cold;
   }
-  __device__ __forceinline__ double value64(int64_t row, int c) const {
+  __device__ __forceinline__ double value64(int64_t row, int c, const uint4 *) const {
     const int64_t at = row * p.out.n + c;
     const uint16_t x = p.x_out ? p.x_out[at]
                                : x64<T>(p.h[at], p.x[at], p.gamma_post + c, gate_row ? gate_row + c : nullptr,

@@ -221,7 +221,7 @@ __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_grou
 // row's end), called by every lane; u < 0 for lanes without a unit.
 template <int NU, class Op, class Use>
 __device__ __forceinline__ void flagged_units(const Op &op, int64_t row, unsigned flags, int first, int step,
-                                              int n, Use &&use) {
+                                              int n, const uint4 *at, Use &&use) {
   const int lane = threadIdx.x & 31, group = lane >> 3;
 #pragma unroll 1
   for (int i = 0; i < NU; ++i) {
@@ -232,7 +232,7 @@ __device__ __forceinline__ void flagged_units(const Op &op, int64_t row, unsigne
       for (int g = 0; g < 4; ++g) who &= who - 1u;
       const int u = mine ? first - lane + (__ffs(mine) - 1) + i * step : -1;
       const int c = 8 * u + (lane & 7);
-      use(u, c, u >= 0 && c < n ? op.value64(row, c) : 0.0);
+      use(u, c, u >= 0 && c < n ? op.value64(row, c, at) : 0.0);
     }
   }
 }
@@ -246,7 +246,10 @@ __device__ __forceinline__ void flagged_units(const Op &op, int64_t row, unsigne
 //   prepare(...)                    the row's statistics
 //   value(row, u, keep, ..., v)     a unit's binary32 values; returns false
 //                                   where they have no error bound
-//   value64(row, c)                 one value in fp64, from memory
+//   value64(row, c, at)             one value in fp64, from memory (or the
+//                                   row's slots at `at`, if not null)
+//   kReadsSlots                     value() reads the slots too, not prepare()
+//                                   alone: the next row is staged later
 //   slack(M)                        bound on |value - value64| over the row
 //   coarse(keep, inv)               bound on the error of a unit's quotients
 template <class Op>
@@ -277,7 +280,8 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
     }
   };
   // f(u, i) sets the lane's flag of a unit; then the flagged units in fp64
-  auto each_flagged = [&](int64_t row, auto &&f, auto &&use) {
+  // (`at`: the row's staged inputs where they are still there)
+  auto each_flagged = [&](int64_t row, const uint4 *at, auto &&f, auto &&use) {
     if (UPT > 0) {
       unsigned flags = 0u;
 #pragma unroll
@@ -286,13 +290,13 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
         if (u < units && f(u, i)) flags |= 1u << i;
       }
       __syncwarp();
-      if (__any_sync(0xFFFFFFFFu, flags != 0u)) flagged_units<NU>(op, row, flags, tid, nt, n, use);
+      if (__any_sync(0xFFFFFFFFu, flags != 0u)) flagged_units<NU>(op, row, flags, tid, nt, n, at, use);
     } else {
       for (int u0 = tid & ~31; u0 < units; u0 += nt) {  // whole warps
         const int u = u0 + (tid & 31);
         const unsigned flags = u < units && f(u, 0) ? 1u : 0u;
         __syncwarp();
-        flagged_units<1>(op, row, flags, u, 0, n, use);
+        flagged_units<1>(op, row, flags, u, 0, n, at, use);
       }
     }
   };
@@ -314,12 +318,12 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
     float2 v[NU][4];
     if (Op::STAGED) copies_wait();
     op.prepare(sm, row, keep, slots + tid, nt, each, nwarps);
+    if (!Op::kReadsSlots) stage(row + gridDim.x);  // prepare() has read them, behind a barrier
 
     if (Op::QT == kQNone) {
-      if (Op::STAGED) stage(row + gridDim.x);  // prepare() has read the slots, behind a barrier
       uint16_t *yr = reinterpret_cast<uint16_t *>(out.y) + row * n;
       each_flagged(
-          row,
+          row, nullptr,
           [&](int u, int i) {
             const bool ok = op.value(row, u, keep[i], slots + i * nt + tid, UPT * nt, v[i]);
             uint32_t w[4];
@@ -341,7 +345,6 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
       top32 = abs_top8(v[i], top32);
     });
     const float M = block_max(top32, sm.top, nwarps);
-    stage(row + gridDim.x);  // the values of this row's slots have met the barrier
     const bool wide = !(M >= kTiny && M <= kHuge);  // the whole row in fp64
     if (tid == 0) sm.cand[parity ^ 1] = 0ull;       // the next row's
 
@@ -350,7 +353,7 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
     if (__any_sync(0xFFFFFFFFu, wide || top32 >= thr)) {
       unsigned long long best = 0ull;
       each_flagged(
-          row,
+          row, Op::STAGED && Op::kReadsSlots ? slots : nullptr,
           [&](int u, int i) {
             if (UPT == 0) op.value(row, u, keep[i], slots, 0, v[i]);
             return wide || abs_max8(v[i]) >= thr;
@@ -361,6 +364,7 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
       if (best) atomicMax(&sm.cand[parity], best);
     }
     __syncthreads();
+    if (Op::kReadsSlots) stage(row + gridDim.x);
     const double top = __longlong_as_double(static_cast<long long>(sm.cand[parity]));
     const float sc = __double2float_rn(wide ? div_ieee(top, static_cast<double>(Q)) : div_q<Q>(top));
     if (tid == 0) out.scale[row] = sc;
@@ -371,7 +375,7 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
     const int64_t code_bytes = Op::QT == 1 ? n / 2 : n;
     uint8_t *yr = out.y + row * code_bytes;
     each_flagged(
-        row,
+        row, nullptr,
         [&](int u, int i) {
           if (UPT == 0) op.value(row, u, keep[i], slots, 0, v[i]);
           // t = value/scale; adding kMagic rounds it to a whole number whose
