@@ -180,60 +180,76 @@ def rms_norm_dynamic_quant(x, gamma, beta=None, smooth=None, *, eps: float = 1e-
 _ACT = {"silu": _abi.ARNQ_SILU, "gelu_tanh": _abi.ARNQ_GELU_TANH}
 
 
+class _Torch:
+    """What the calls below use of torch, looked up once: a decode step makes
+    many small calls, and their host time is what it waits for."""
+
+    def __init__(self):
+        import torch
+        self.empty = torch.empty
+        self.Tensor = torch.Tensor
+        self.int8, self.uint8, self.int32 = torch.int8, torch.uint8, torch.int32
+        self.float32, self.bfloat16 = torch.float32, torch.bfloat16
+        self.dt = {torch.bfloat16: _abi.ARNQ_BF16, torch.float16: _abi.ARNQ_FP16}
+        self.out = {**self.dt, torch.float32: _abi.ARNQ_FP32}
+        self.current_device = torch.cuda.current_device
+        # the current stream's handle without building a Stream object
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
+        self.cuda = torch.cuda
+
+
+_torch_cache = None
+
+
+def _torch():
+    global _torch_cache
+    if _torch_cache is None:
+        _torch_cache = _Torch()
+    return _torch_cache
+
+
 def _operand(t, name, device, dtype, shape=None):
-    """Checks a tensor against the first one's device and a dtype (and shape)."""
+    """Checks a tensor: CUDA, contiguous, on `device`, of `dtype` (and shape)."""
+    try:
+        if (t.dtype is dtype and t.device == device and t.is_contiguous() and
+                (shape is None or t.shape == shape)):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _check(t, name, dtype)
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _call(entry, args, device, stream, outputs, workspace_bytes=0):
-    """Allocates the outputs not given (on the stream the call runs on) and
-    calls a C entry point with the tensors' device current.
-
-    outputs: list of (given tensor or None, name, shape, dtype), or None for an output
-    that the call does not have; returns the output tensors.  `args` builds
-    the entry's arguments from (pointers of the outputs, workspace, stream)."""
-    import torch
-
-    def go():
-        made = []
-        for o in outputs:
-            if o is None:
-                made.append(None)
-                continue
-            given, name, shape, dtype = o
-            if given is not None:
-                _operand(given, name, device, dtype, shape)
-            else:
-                given = torch.empty(shape, dtype=dtype, device=device)
-            made.append(given)
-        ws = workspace(device, workspace_bytes, stream) if workspace_bytes else None
-        st = getattr(_abi, entry)(*args(made, ws, stream))
-        if st != _abi.ARNQ_OK:
-            raise ArnqError(st, entry)
-        return made
-
-    current = torch.cuda.current_device() == device.index
+def _on_stream(call, device, stream):
+    """call(handle of the stream to launch on), with `device` and that stream
+    current: outputs allocated inside belong to the stream they are made on."""
+    T = _torch()
     if stream is None:
-        if current:
-            stream = torch.cuda.current_stream(device)
-            return go()
-        with torch.cuda.device(device):
-            stream = torch.cuda.current_stream(device)
-            return go()
+        if T.current_device() == device.index:
+            return call(T.raw_stream(device.index))
+        with T.cuda.device(device):
+            return call(T.raw_stream(device.index))
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
+        stream = T.cuda.ExternalStream(stream, device=device)
     if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, not on {device}")
-    with torch.cuda.stream(stream):  # the device too; outputs belong to this stream
-        return go()
+    with T.cuda.stream(stream):  # (the device too)
+        return call(stream.cuda_stream)
 
 
-_OUT = {"torch.bfloat16": _abi.ARNQ_BF16, "torch.float16": _abi.ARNQ_FP16,
-        "torch.float32": _abi.ARNQ_FP32}
+_status_blocks = {}
+
+
+def _status_block(device, stream: int) -> int:
+    """Address of the workspace of calls that only need the status block."""
+    key = (device.index, stream)
+    kept = _status_blocks.get(key)
+    if kept is None:
+        ws = workspace(device, _abi.ARNQ_WORKSPACE_BYTES, stream)
+        kept = _status_blocks[key] = (ws.data_ptr(), ws)
+    return kept[0]
 
 
 def quant_matmul(x, scale_x, w, scale_w, bias=None, *, out_dtype=None, stream=None, out=None):
@@ -246,29 +262,62 @@ def quant_matmul(x, scale_x, w, scale_w, bias=None, *, out_dtype=None, stream=No
     bias: [n] of the output dtype.  out_dtype: torch.bfloat16 (the default),
     float16 or float32; `out` may pass y [..., n] preallocated.
     """
-    import torch
-    _check(x, "x", torch.int8)
-    device = x.device
+    T = _torch()
+    _check(x, "x", T.int8)
+    device, shape = x.device, x.shape
     if out_dtype is None:
-        out_dtype = torch.bfloat16
-    code = _OUT.get(str(out_dtype))
+        out_dtype = T.bfloat16
+    code = T.out.get(out_dtype)
     if code is None:
         raise ValueError(f"unsupported out_dtype {out_dtype}")
-    lead, k = tuple(x.shape[:-1]), x.shape[-1] if x.dim() else 0
-    _operand(w, "w", device, torch.int8)
+    if not shape:
+        raise ValueError("x must have at least one dimension")
+    lead, k = shape[:-1], shape[-1]
+    pw = _operand(w, "w", device, T.int8)
     if w.dim() != 2 or w.shape[1] != k:
         raise ValueError(f"w must have shape [n, {k}], got {tuple(w.shape)}")
     n = w.shape[0]
-    m = x.numel() // k if k else 0
-    _operand(scale_x, "scale_x", device, torch.float32, lead)
-    _operand(scale_w, "scale_w", device, torch.float32, (n,))
-    if bias is not None:
-        _operand(bias, "bias", device, out_dtype, (n,))
-    return _call(
-        "arnq_quant_matmul",
-        lambda o, ws, st: (x, scale_x, w, scale_w, bias, m, n, k, code, o[0], ws, ws.numel(), st),
-        device, stream, [(out, "out", lead + (n,), out_dtype)],
-        workspace_bytes=_abi.ARNQ_WORKSPACE_BYTES)[0]
+    psx = _operand(scale_x, "scale_x", device, T.float32, lead)
+    psw = _operand(scale_w, "scale_w", device, T.float32, (n,))
+    pb = None if bias is None else _operand(bias, "bias", device, out_dtype, (n,))
+    oshape = (*lead, n)
+
+    def call(s):
+        y = out
+        if y is None:
+            y = T.empty(oshape, dtype=out_dtype, device=device)
+            py = y.data_ptr()
+        else:
+            py = _operand(y, "out", device, out_dtype, oshape)
+        st = _abi.lib().arnq_quant_matmul(
+            x.data_ptr(), psx, pw, psw, pb, x.numel() // k if k else 0, n, k, code, py,
+            _status_block(device, s), _abi.ARNQ_WORKSPACE_BYTES, s)
+        if st != _abi.ARNQ_OK:
+            raise ArnqError(st, "arnq_quant_matmul")
+        return y
+
+    return _on_stream(call, device, stream)
+
+
+def _outputs(given, specs, device):
+    """Tensors and addresses of a call's outputs: those given (checked) or new
+    ones.  specs: (name, shape, dtype), or None for one the call has not."""
+    T = _torch()
+    made, at = [], []
+    for spec in specs:
+        if spec is None:
+            made.append(None)
+            at.append(None)
+            continue
+        name, shape, dtype = spec
+        t = given.get(name) if given else None
+        if t is None:
+            t = T.empty(shape, dtype=dtype, device=device)
+            at.append(t.data_ptr())
+        else:
+            at.append(_operand(t, name, device, dtype, shape))
+        made.append(t)
+    return made, at
 
 
 def post_norm_add_rms_norm_dynamic_quant(h, x, gamma_post, gamma, beta=None, gate=None, smooth=None,
@@ -293,42 +342,45 @@ def post_norm_add_rms_norm_dynamic_quant(h, x, gamma_post, gamma, beta=None, gat
     inputs' dtype and scale None.  eps_post defaults to eps.  `out` may pass
     preallocated tensors under the keys y, scale, x_out; x_out may be x.
     """
+    T = _torch()
     _check(x, "x")
-    dt, device, n = x.dtype, x.device, x.shape[-1] if x.dim() else 0
-    code = _DT.get(str(dt))
+    dt, device, shape = x.dtype, x.device, x.shape
+    code = T.dt.get(dt)
     if code is None:
         raise ValueError(f"unsupported dtype {dt}")
-    rows = x.numel() // n if n else 0
-    _operand(h, "h", device, dt, x.shape)
-    for name, t in (("gamma_post", gamma_post), ("gamma", gamma)):
-        _operand(t, name, device, dt, (n,))
-    for name, t in (("beta", beta), ("smooth", smooth)):
-        if t is not None:
-            _operand(t, name, device, dt, (n,))
-    gate_rows = 0
+    if not shape:
+        raise ValueError("x must have at least one dimension")
+    n, lead = shape[-1], shape[:-1]
+    vec = (n,)
+    ph = _operand(h, "h", device, dt, shape)
+    pgp = _operand(gamma_post, "gamma_post", device, dt, vec)
+    pg = _operand(gamma, "gamma", device, dt, vec)
+    pb = None if beta is None else _operand(beta, "beta", device, dt, vec)
+    ps = None if smooth is None else _operand(smooth, "smooth", device, dt, vec)
+    pgate, gate_rows = None, 0
     if gate is not None:
-        _operand(gate, "gate", device, dt)
+        pgate = _operand(gate, "gate", device, dt)
         if gate.dim() < 1 or gate.shape[-1] != n:
             raise ValueError(f"gate must have shape [{n}] or [g, {n}], got {tuple(gate.shape)}")
         gate_rows = gate.numel() // n if n else 0
-    lead = tuple(x.shape[:-1])
     if qdtype is None:
-        q, cshape, cdt = _abi.ARNQ_NO_CODES, tuple(x.shape), dt
+        q, specs = _abi.ARNQ_NO_CODES, [("y", shape, dt), None, ("x_out", shape, dt)]
     else:
         cshape, cdt = _codes_like(lead, n, qdtype)
         q = _QDT[qdtype]
-    given = out or {}
-    import torch
-    y, scale, x_out = _call(
-        "arnq_post_norm_add_rms_norm_dynamic_quant",
-        lambda o, ws, st: (h, x, gamma_post, gate, gate_rows, residual_scale, gamma, beta, smooth,
-                           rows, n, code, eps if eps_post is None else eps_post, eps, q, o[0],
-                           o[1], o[2], st),
-        device, stream,
-        [(given.get("y"), "y", cshape, cdt),
-         None if qdtype is None else (given.get("scale"), "scale", lead, torch.float32),
-         (given.get("x_out"), "x_out", tuple(x.shape), dt)])
-    return y, scale, x_out
+        specs = [("y", cshape, cdt), ("scale", lead, T.float32), ("x_out", shape, dt)]
+
+    def call(s):
+        made, at = _outputs(out, specs, device)
+        st = _abi.lib().arnq_post_norm_add_rms_norm_dynamic_quant(
+            ph, x.data_ptr(), pgp, pgate, gate_rows, residual_scale, pg, pb, ps,
+            x.numel() // n if n else 0, n, code, eps if eps_post is None else eps_post, eps, q,
+            at[0], at[1], at[2], s)
+        if st != _abi.ARNQ_OK:
+            raise ArnqError(st, "arnq_post_norm_add_rms_norm_dynamic_quant")
+        return tuple(made)
+
+    return _on_stream(call, device, stream)
 
 
 def glu_dynamic_quant(x, smooth=None, *, activation: str = "silu", qdtype: str = "int8",
@@ -342,27 +394,29 @@ def glu_dynamic_quant(x, smooth=None, *, activation: str = "silu", qdtype: str =
     x: [..., 2n] bf16 or fp16; smooth: [n] same dtype; activation "silu" or
     "gelu_tanh".  Returns (y, scale); `out` may pass them preallocated.
     """
+    T = _torch()
     _check(x, "x")
-    dt, device = x.dtype, x.device
-    code = _DT.get(str(dt))
+    dt, device, shape = x.dtype, x.device, x.shape
+    code = T.dt.get(dt)
     if code is None:
         raise ValueError(f"unsupported dtype {dt}")
-    if activation not in _ACT:
+    act = _ACT.get(activation)
+    if act is None:
         raise ValueError(f"unknown activation {activation!r}")
-    two_n = x.shape[-1] if x.dim() else 0
-    if two_n % 2:
-        raise ValueError(f"x must have an even last dimension (gate and up), got {two_n}")
-    n = two_n // 2
-    rows = x.numel() // two_n if n else 0
-    if smooth is not None:
-        _operand(smooth, "smooth", device, dt, (n,))
-    lead = tuple(x.shape[:-1])
+    if not shape or shape[-1] % 2:
+        raise ValueError(f"x must have an even last dimension (gate and up), got {tuple(shape)}")
+    n, lead = shape[-1] // 2, shape[:-1]
+    ps = None if smooth is None else _operand(smooth, "smooth", device, dt, (n,))
     cshape, cdt = _codes_like(lead, n, qdtype)
-    given = out or {}
-    import torch
-    y, scale = _call(
-        "arnq_glu_dynamic_quant",
-        lambda o, ws, st: (x, smooth, rows, n, code, _ACT[activation], _QDT[qdtype], o[0], o[1], st),
-        device, stream,
-        [(given.get("y"), "y", cshape, cdt), (given.get("scale"), "scale", lead, torch.float32)])
-    return y, scale
+    specs = [("y", cshape, cdt), ("scale", lead, T.float32)]
+
+    def call(s):
+        made, at = _outputs(out, specs, device)
+        st = _abi.lib().arnq_glu_dynamic_quant(
+            x.data_ptr(), ps, x.numel() // (2 * n) if n else 0, n, code, act, _QDT[qdtype], at[0],
+            at[1], s)
+        if st != _abi.ARNQ_OK:
+            raise ArnqError(st, "arnq_glu_dynamic_quant")
+        return tuple(made)
+
+    return _on_stream(call, device, stream)

@@ -10,7 +10,8 @@ constexpr int kDevices = 64;
 constexpr int kEntries = 256;
 struct Entry {
   const void *fn;
-  int dev, threads, smem, per_sm;
+  int dev, threads, smem, cluster;  // cluster: 0 for CTAs per SM
+  int count;
 };
 std::mutex g_mutex;
 int g_sms[kDevices];       // 0: not looked up yet
@@ -32,13 +33,13 @@ arnq_status current_device(int *dev, int *sms) {
   return ARNQ_OK;
 }
 
-arnq_status resident_ctas(const void *fn, int dev, int threads, int smem, int *per_sm) {
+static arnq_status resident(const void *fn, int dev, int threads, int smem, int cluster, int *count) {
   std::lock_guard<std::mutex> lock(g_mutex);
   const int have = g_count < kEntries ? g_count : kEntries;
   for (int i = 0; i < have; ++i) {
     const Entry &e = g_entries[i];
-    if (e.fn == fn && e.dev == dev && e.threads == threads && e.smem == smem) {
-      *per_sm = e.per_sm;
+    if (e.fn == fn && e.dev == dev && e.threads == threads && e.smem == smem && e.cluster == cluster) {
+      *count = e.count;
       return ARNQ_OK;
     }
   }
@@ -52,15 +53,37 @@ arnq_status resident_ctas(const void *fn, int dev, int threads, int smem, int *p
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, limit) != cudaSuccess)
       return ARNQ_ERR_CUDA;
   }
-  int ctas = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, fn, threads, smem) != cudaSuccess ||
-      ctas < 1)
-    return ARNQ_ERR_CUDA;
-  g_entries[g_count % kEntries] = Entry{fn, dev, threads, smem, ctas};
+  int found = 0;
+  if (cluster == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&found, fn, threads, smem) != cudaSuccess)
+      return ARNQ_ERR_CUDA;
+  } else {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(cluster * 1024, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&found, fn, &cfg) != cudaSuccess) return ARNQ_ERR_CUDA;
+  }
+  if (found < 1) return ARNQ_ERR_CUDA;
+  g_entries[g_count % kEntries] = Entry{fn, dev, threads, smem, cluster, found};
   ++g_count;
   if (g_count >= 2 * kEntries) g_count -= kEntries;
-  *per_sm = ctas;
+  *count = found;
   return ARNQ_OK;
+}
+
+arnq_status resident_ctas(const void *fn, int dev, int threads, int smem, int *per_sm) {
+  return resident(fn, dev, threads, smem, 0, per_sm);
+}
+arnq_status resident_clusters(const void *fn, int dev, int threads, int smem, int cluster, int *clusters) {
+  return resident(fn, dev, threads, smem, cluster, clusters);
 }
 
 arnq_status launch_dependent(const void *fn, dim3 grid, int threads, int smem, int cluster,

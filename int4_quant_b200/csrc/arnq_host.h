@@ -22,6 +22,9 @@ arnq_status current_device(int *dev, int *sms);
 // first.  Looked up once per (fn, dev, threads, smem).
 arnq_status resident_ctas(const void *fn, int dev, int threads, int smem, int *per_sm);
 
+// Clusters of `cluster` CTAs of `fn` resident on `dev` at once.
+arnq_status resident_clusters(const void *fn, int dev, int threads, int smem, int cluster, int *clusters);
+
 // Launches as a programmatic dependent of the preceding work on the stream,
 // in clusters of `cluster` CTAs.
 arnq_status launch_dependent(const void *fn, dim3 grid, int threads, int smem, int cluster,

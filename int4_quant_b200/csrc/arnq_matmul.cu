@@ -40,8 +40,25 @@ bool encode(CUtensorMap *map, const void *p, int64_t rows, int64_t k, int box_ro
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// output rows [m, n] in boxes of 32 rows x 128 bytes, 128-byte swizzled
+bool encode_out(CUtensorMap *map, void *y, int64_t m, int64_t n, int out) {
+  const EncodeFn f = encode_fn();
+  if (!f) return false;
+  const cuuint64_t esz = out == ARNQ_FP32 ? 4 : 2;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(m)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(n) * esz};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / esz), 32};
+  const cuuint32_t one[2] = {1, 1};
+  const CUtensorMapDataType type = out == ARNQ_FP32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : out == ARNQ_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return f(map, type, 2, y, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr int kSmemLimit = 227 * 1024;
-constexpr int kStatic = 1024;  // the kernels' static shared memory, rounded up
+constexpr int kStatic = 2048;  // the kernels' static shared memory, rounded up
 
 arnq_status launch_split(MatmulParams &p, bool plain, int sms, int dev, cudaStream_t stream) {
   const int64_t token_tiles = div_up(p.m, 256);
@@ -72,6 +89,23 @@ arnq_status launch_split(MatmulParams &p, bool plain, int sms, int dev, cudaStre
   if (st != ARNQ_OK) return st;
   return launch_dependent(fn, dim3(static_cast<unsigned>(tiles * token_tiles * split)), kSplitThreads,
                           smem, split, stream, &p);
+}
+
+arnq_status launch_pair(MatmulParams &p, int dev, cudaStream_t stream) {
+  p.token_tiles = static_cast<int32_t>(div_up(p.m, 256));
+  p.channel_tiles = static_cast<int32_t>(div_up(p.n, 256));
+  const int esz = p.out == ARNQ_FP32 ? 4 : 2;
+  p.tma_out = p.n * esz % 16 == 0 && is_aligned(p.y, 16) ? 1 : 0;
+  if (!encode(&p.map_w, p.w, p.n, p.k, 128) || !encode(&p.map_x, p.x, p.m, p.k, 128) ||
+      (p.tma_out && !encode_out(&p.map_y, p.y, p.m, p.n, p.out)))
+    return ARNQ_ERR_CUDA;
+  const void *fn = reinterpret_cast<const void *>(matmul_pair_kernel);
+  int pairs = 0;
+  const arnq_status st = resident_clusters(fn, dev, kPairThreads, kPairSmem, 2, &pairs);
+  if (st != ARNQ_OK) return st;
+  const int64_t tiles = static_cast<int64_t>(p.token_tiles) * p.channel_tiles;
+  if (tiles < pairs) pairs = static_cast<int>(tiles);
+  return launch_dependent(fn, dim3(2 * pairs), kPairThreads, kPairSmem, 2, stream, &p);
 }
 
 }  // namespace
@@ -108,5 +142,6 @@ extern "C" arnq_status arnq_quant_matmul(const void *x, const float *scale_x, co
   p.vec_out = n % 4 == 0 && is_aligned(y, 4 * esz) ? 1 : 0;
   p.wait_limit_ns = kWaitLimitNs;
   const bool plain = k % 16 != 0 || !is_aligned(x, 16) || !is_aligned(w, 16);
+  if (!plain && m > 512) return launch_pair(p, dev, static_cast<cudaStream_t>(stream));
   return launch_split(p, plain, sms, dev, static_cast<cudaStream_t>(stream));
 }

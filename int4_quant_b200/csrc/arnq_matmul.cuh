@@ -14,6 +14,7 @@
 namespace arnq {
 
 struct MatmulParams {
+  CUtensorMap map_y;         // pair kernel: the output
   CUtensorMap map_w, map_x;  // tensor maps of the codes (not used by the plain-load variant)
   const int8_t *x, *w;
   const float *scale_x, *scale_w;
@@ -23,8 +24,10 @@ struct MatmulParams {
   int64_t m, n, k;
   int32_t out;       // 0 bf16, 1 fp16, 2 fp32
   int32_t vec_out;   // y rows take vector stores
+  int32_t tma_out;   // pair kernel: the output goes through map_y
+  int32_t token_tiles;    // pair kernel: tiles of 256 tokens
   int32_t tokens;    // split kernel: token rows a tile holds (a multiple of 16)
-  int32_t channel_tiles;  // split kernel: tiles of 128 channels
+  int32_t channel_tiles;  // tiles of 128 (split kernel) or 256 (pair kernel) channels
   int32_t split;     // split kernel: CTAs (one cluster) sharing a tile's K
   int32_t stages;
   uint32_t tmem_cols;
@@ -144,6 +147,7 @@ __global__ void __launch_bounds__(kSplitThreads) matmul_split_kernel(const __gri
   __shared__ __align__(8) uint64_t full[kSplitMaxStages], empty[kSplitMaxStages], done;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
+  __shared__ float sx[256];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_addr(dyn) + 1023u) & ~1023u;
   unsigned char *base_ptr = dyn + (base - smem_addr(dyn));
@@ -176,6 +180,18 @@ __global__ void __launch_bounds__(kSplitThreads) matmul_split_kernel(const __gri
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // what the epilogue needs besides the sums, fetched while they form
+  const int count = static_cast<int>(p.m - t0 < p.tokens ? p.m - t0 : p.tokens);
+  const int64_t c = c0 + lane * 4;
+  const int have = static_cast<int>(p.n - c < 0 ? 0 : p.n - c < 4 ? p.n - c : 4);
+  float sw[4], b[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    sw[j] = j < have ? p.scale_w[c + j] : 0.f;
+    b[j] = j < have ? load_bias(p, c + j) : 0.f;
+  }
+  for (int t = tid - 64; t >= 0 && t < count; t += 128) sx[t] = p.scale_x[t0 + t];
 
   // every wait is bounded; whoever gives up tells the others
   auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
@@ -235,7 +251,6 @@ __global__ void __launch_bounds__(kSplitThreads) matmul_split_kernel(const __gri
 
   // ---- partial sums to shared memory: part[t][channel], over the stages
   int32_t *part = reinterpret_cast<int32_t *>(base_ptr);
-  const int count = static_cast<int>(p.m - t0 < p.tokens ? p.m - t0 : p.tokens);
   if (warp >= 2) {
     const bool ok = wait(&done, 0);
     tc_fence_after();
@@ -261,35 +276,273 @@ __global__ void __launch_bounds__(kSplitThreads) matmul_split_kernel(const __gri
   const bool failed = abort_flag != 0;
   if (failed && tid == 0) report_timeout(p.status);
 
-  // ---- sums over the cluster, scales, output: a warp a token, four channels a lane
-  if (!failed) {
-    const int64_t c = c0 + lane * 4;
-    const int have = static_cast<int>(p.n - c < 0 ? 0 : p.n - c < 4 ? p.n - c : 4);
-    float sw[4], b[4];
+  // ---- sums over the cluster, scales, output: a warp a token, four channels a
+  // lane, four tokens at a time
+  if (!failed && have > 0) {
+    constexpr int kStep = kSplitThreads / 32;
+    for (int t = rank + warp * split; t < count; t += 4 * split * kStep) {
+      int4 sum[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      sw[j] = j < have ? p.scale_w[c + j] : 0.f;
-      b[j] = j < have ? load_bias(p, c + j) : 0.f;
-    }
-    for (int t = rank + warp * split; t < count; t += split * (kSplitThreads / 32)) {
-      int4 sum = make_int4(0, 0, 0, 0);
+      for (int g = 0; g < 4; ++g) sum[g] = make_int4(0, 0, 0, 0);
       for (int r = 0; r < split; ++r) {
-        const int4 v = *reinterpret_cast<const int4 *>(
-            cluster.map_shared_rank(part + t * 128 + lane * 4, r));
-        sum.x += v.x;
-        sum.y += v.y;
-        sum.z += v.z;
-        sum.w += v.w;
+        const int32_t *from = cluster.map_shared_rank(part, r) + lane * 4;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int tg = t + g * split * kStep;
+          if (tg >= count) continue;
+          const int4 v = *reinterpret_cast<const int4 *>(from + tg * 128);
+          sum[g].x += v.x;
+          sum[g].y += v.y;
+          sum[g].z += v.z;
+          sum[g].w += v.w;
+        }
       }
-      const float sx = p.scale_x[t0 + t];
-      const float v[4] = {__fmaf_rn(__int2float_rn(sum.x) * sx, sw[0], b[0]),
-                          __fmaf_rn(__int2float_rn(sum.y) * sx, sw[1], b[1]),
-                          __fmaf_rn(__int2float_rn(sum.z) * sx, sw[2], b[2]),
-                          __fmaf_rn(__int2float_rn(sum.w) * sx, sw[3], b[3])};
-      if (have > 0) store4(p, (t0 + t) * p.n + c, v, have);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int tg = t + g * split * kStep;
+        if (tg >= count) continue;
+        const float f = sx[tg];
+        const float v[4] = {__fmaf_rn(__int2float_rn(sum[g].x) * f, sw[0], b[0]),
+                            __fmaf_rn(__int2float_rn(sum[g].y) * f, sw[1], b[1]),
+                            __fmaf_rn(__int2float_rn(sum[g].z) * f, sw[2], b[2]),
+                            __fmaf_rn(__int2float_rn(sum[g].w) * f, sw[3], b[3])};
+        store4(p, (t0 + tg) * p.n + c, v, have);
+      }
     }
   }
   cluster.sync();  // nobody leaves while its partial sums are being read
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// ------------------------------------------------------------ many tokens
+
+// Output tiles of 256 tokens x 256 channels by pairs of CTAs (cta_group::2):
+// each CTA brings 128 tokens and 128 channels of a stage, one thread of the
+// pair's first CTA issues the MMAs of both, and each CTA holds its 128 tokens
+// (TMEM lanes) by 256 channels (columns), twice: one tile's sums are turned into
+// outputs while the next one's are formed.  A pair is what halves the shared
+// memory traffic of an SM (per 32 codes of K: 8 KB read and 8 KB written in
+// the 128 cycles of its MMA, where a CTA alone would need 12 + 12 KB and the
+// SM moves 128 bytes a cycle).  Persistent: pair i takes tiles i, i + pairs, ...
+// in groups of eight token tiles, so that the pairs at work share operands in L2.
+// Warps: 0 copies, 1 MMA and TMEM, 2-5 the epilogue: a thread has a token's
+// row, scales it (token scale in a register, channel scales and bias from the
+// warp's shared memory), packs 128 bytes of it into the warp's swizzled buffer
+// and sends 32 rows of them as one tensor-map store (or, for rows that tensor
+// maps cannot describe, element by element).
+constexpr int kPairThreads = 192;
+constexpr int kPairStages = 5;
+constexpr int kPairStageBytes = 32768;  // 128 tokens and 128 channels
+constexpr int kPairGroup = 8;
+constexpr int kPairSmem = kPairStages * kPairStageBytes + 4 * 2 * 4096 + 4 * 2048 + 1024;
+
+__global__ void __launch_bounds__(kPairThreads) matmul_pair_kernel(const __grid_constant__ MatmulParams p) {
+  namespace cg = cooperative_groups;
+  extern __shared__ unsigned char dyn[];
+  __shared__ __align__(8) uint64_t full[kPairStages], empty[kPairStages], acc_full[2], acc_empty[2], drained;
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  cg::cluster_group cluster = cg::this_cluster();
+  const uint32_t rank = cluster.block_rank();
+  const uint32_t base = (smem_addr(dyn) + 1023u) & ~1023u;
+  const int pairs = static_cast<int>(gridDim.x) >> 1;
+  const int64_t tiles = static_cast<int64_t>(p.token_tiles) * p.channel_tiles;
+  const int chunks = static_cast<int>((p.k + kTileK - 1) / kTileK);
+
+  if (tid == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(smem_addr(&full[s]), 1);
+      mbar_init(smem_addr(&empty[s]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&acc_full[i]), 1);
+      mbar_init(smem_addr(&acc_empty[i]), 8);  // the epilogue warps of both CTAs
+    }
+    mbar_init(smem_addr(&drained), 1);
+    abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tma_prefetch_map(&p.map_w);
+    tma_prefetch_map(&p.map_x);
+    if (p.tma_out) tma_prefetch_map(&p.map_y);
+  }
+  if (warp == 1) tmem_alloc<2>(smem_addr(&tmem_slot), 512);
+  tc_fence_before();
+  cluster.sync();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // every wait is bounded; whoever gives up tells this CTA's others (the peer's
+  // waits run out too)
+  auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+    if (abort_flag) return false;
+    if (mbar_wait_bounded(smem_addr(bar), parity, p.wait_limit_ns)) return true;
+    abort_flag = 1;
+    return false;
+  };
+  // tile i of the pair -> (token tile, channel tile)
+  auto tile_at = [&](int64_t t, int64_t *t0, int64_t *c0) {
+    const int64_t group = static_cast<int64_t>(kPairGroup) * p.channel_tiles;
+    const int64_t first = t / group * kPairGroup, in = t % group;
+    const int64_t size = p.token_tiles - first < kPairGroup ? p.token_tiles - first : kPairGroup;
+    *t0 = (first + in % size) * 256;
+    *c0 = in / size * 256;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int64_t i = 0;  // stages filled so far
+      bool ok = true;
+      for (int64_t t = blockIdx.x >> 1; ok && t < tiles; t += pairs) {
+        int64_t t0, c0;
+        tile_at(t, &t0, &c0);
+        for (int kc = 0; kc < chunks; ++kc, ++i) {
+          const int s = static_cast<int>(i % kPairStages);
+          if (i >= kPairStages && !wait(&empty[s], (static_cast<uint32_t>(i / kPairStages) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          // both CTAs' copies complete on the first one's barrier
+          if (rank == 0) mbar_arrive_expect_tx(smem_addr(&full[s]), 2 * kPairStageBytes);
+          const uint32_t bar = peer_addr(smem_addr(&full[s]), 0), at = base + s * kPairStageBytes;
+          tma_2d_pair(at, &p.map_x, kc * kTileK, static_cast<int>(t0 + rank * 128), bar);
+          tma_2d_pair(at + 16384, &p.map_w, kc * kTileK, static_cast<int>(c0 + rank * 128), bar);
+        }
+      }
+      if (abort_flag && rank == 0)  // copies still in flight must land before the pair ends
+        for (int64_t j = i > kPairStages ? i - kPairStages : 0; j < i; ++j)
+          mbar_wait_bounded(smem_addr(&full[j % kPairStages]), static_cast<uint32_t>(j / kPairStages) & 1,
+                            p.wait_limit_ns);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc = i8_instr_desc(256, 256);
+      int64_t i = 0;
+      int n_tile = 0;
+      bool ok = true;
+      for (int64_t t = blockIdx.x >> 1; ok && t < tiles; t += pairs, ++n_tile) {
+        const int buf = n_tile & 1;
+        if (n_tile >= 2 && !wait(&acc_empty[buf], ((n_tile >> 1) & 1) ^ 1)) break;
+        tc_fence_after();
+        for (int kc = 0; kc < chunks; ++kc, ++i) {
+          const int s = static_cast<int>(i % kPairStages);
+          if (!wait(&full[s], static_cast<uint32_t>(i / kPairStages) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t a = smem_desc(base + s * kPairStageBytes);
+          const uint64_t b = smem_desc(base + s * kPairStageBytes + 16384);
+#pragma unroll
+          for (int j = 0; j < kTileK / kMmaK; ++j)
+            mma_i8<2>(tmem + buf * 256, a + 2 * j, b + 2 * j, idesc, kc > 0 || j > 0);
+          mma_commit_pair(smem_addr(&empty[s]));
+        }
+        if (ok) mma_commit_pair(smem_addr(&acc_full[buf]));
+      }
+      if (abort_flag) {  // MMAs still at work must end before TMEM is freed
+        mma_commit_pair(smem_addr(&drained));
+        mbar_wait_bounded(smem_addr(&drained), 0, p.wait_limit_ns);
+      }
+    }
+  } else {
+    const int quarter = warp & 3;
+    const uint32_t buffers = base + kPairStages * kPairStageBytes + (warp - 2) * 8192;
+    float *sw = reinterpret_cast<float *>(dyn + (base - smem_addr(dyn)) + kPairStages * kPairStageBytes +
+                                          4 * 8192 + (warp - 2) * 2048);
+    float *bias = sw + 256;
+    const int esz = p.out == 2 ? 4 : 2, cols = 128 / esz;  // columns of 128 bytes
+    int n_tile = 0, sent = 0;
+    for (int64_t t = blockIdx.x >> 1; t < tiles; t += pairs, ++n_tile) {
+      int64_t t0, c0;
+      tile_at(t, &t0, &c0);
+      const int buf = n_tile & 1;
+      const int64_t row = t0 + rank * 128 + quarter * 32 + lane;
+      __syncwarp();
+      for (int j = lane; j < 256; j += 32) {
+        const bool in = c0 + j < p.n;
+        sw[j] = in ? p.scale_w[c0 + j] : 0.f;
+        bias[j] = in ? load_bias(p, c0 + j) : 0.f;
+      }
+      const float sx = row < p.m ? p.scale_x[row] : 0.f;
+      __syncwarp();
+      const bool ok = wait(&acc_full[buf], (n_tile >> 1) & 1);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      tc_fence_after();
+      for (int col = 0; col < 256; col += 32) {
+        int32_t r[32];
+        tmem_ld32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * 256 + col, r);
+        tmem_ld_wait();
+        if (col == 224) {  // this warp has read its part of the tile
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(peer_addr(smem_addr(&acc_empty[buf]), 0));
+        }
+        // a new 128-byte buffer: the store before last must have read it
+        const uint32_t at = buffers + (sent & 1) * 4096 + lane * 128;
+        const int chunk0 = (col % cols) * esz / 16;
+        if (chunk0 == 0) {
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {  // 8 columns: 16 bytes, or 32 of binary32
+          float f[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            f[j] = __fmaf_rn(__int2float_rn(r[8 * q + j]) * sx, sw[col + 8 * q + j], bias[col + 8 * q + j]);
+          if (p.out == 2) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               at + (((chunk0 + 2 * q + h) ^ (lane & 7)) << 4)),
+                           "r"(__float_as_uint(f[4 * h])), "r"(__float_as_uint(f[4 * h + 1])),
+                           "r"(__float_as_uint(f[4 * h + 2])), "r"(__float_as_uint(f[4 * h + 3]))
+                           : "memory");
+          } else {
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             at + (((chunk0 + q) ^ (lane & 7)) << 4)),
+                         "r"(pack_out(p, f[0], f[1])), "r"(pack_out(p, f[2], f[3])),
+                         "r"(pack_out(p, f[4], f[5])), "r"(pack_out(p, f[6], f[7]))
+                         : "memory");
+          }
+        }
+        if ((col + 32) % cols != 0) continue;
+        // 128 bytes of 32 rows are ready
+        const int64_t c = c0 + col + 32 - cols, first = row - lane;
+        if (p.tma_out) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            if (c < p.n && first < p.m)
+              tma_store_2d(&p.map_y, static_cast<int>(c), static_cast<int>(first),
+                           buffers + (sent & 1) * 4096);
+            bulk_commit();  // (an empty group too: the waits count groups)
+          }
+        } else {
+          __syncwarp();
+          const unsigned char *from = dyn + (buffers + (sent & 1) * 4096 - smem_addr(dyn));
+          for (int r2 = 0; r2 < 32 && first + r2 < p.m; ++r2)
+            for (int j = lane; j < cols && c + j < p.n; j += 32) {
+              const unsigned char *e = from + r2 * 128 + (((j * esz / 16) ^ (r2 & 7)) << 4) + (j * esz) % 16;
+              const int64_t o = (first + r2) * p.n + c + j;
+              if (esz == 4) static_cast<uint32_t *>(p.y)[o] = *reinterpret_cast<const uint32_t *>(e);
+              else static_cast<uint16_t *>(p.y)[o] = *reinterpret_cast<const uint16_t *>(e);
+            }
+          __syncwarp();
+        }
+        ++sent;
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster.sync();  // neither leaves while the other reads its memory or signals it
+  tc_fence_after();
+  if (warp == 1) tmem_release<2>(tmem, 512);
+  if (abort_flag && tid == 0) report_timeout(p.status);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 

@@ -198,3 +198,28 @@ def test_block_of_operators():
     torch.cuda.synchronize()
     for p, q in zip(got, again):
         assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("m,n,k", [(513, 256, 128), (700, 300, 640), (1024, 1000, 4096), (2048, 777, 1040),
+                                   (5000, 264, 144), (1500, 4104, 2048), (3000, 8, 16), (520, 16384, 256)])
+def test_many_tokens(m, n, k, out):
+    run(m, n, k, out, True, seed=m + n)
+
+
+def test_many_tokens_output_off_alignment():
+    x, sx, w, sw, _ = case(800, 512, 256, seed=4)
+    buf = torch.full((800 * 512 + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = buf[33:33 + 800 * 512].view(800, 512)
+    lib.quant_matmul(x, sx, w, sw, out=y)
+    check(x, sx, w, sw, None, y)
+    assert (buf[:33] == 7).all() and (buf[33 + 800 * 512:] == 7).all()
+
+
+def test_many_tokens_leaves_neighbours_alone():
+    # ragged rows and channels of an aligned output inside a larger buffer
+    x, sx, w, sw, _ = case(777, 264, 256, seed=8)
+    buf = torch.full((1000, 264), 7.0, dtype=torch.bfloat16, device="cuda")
+    lib.quant_matmul(x, sx, w, sw, out=buf[:777])
+    check(x, sx, w, sw, None, buf[:777])
+    assert (buf[777:] == 7).all()
