@@ -195,8 +195,8 @@ __global__ void __launch_bounds__(kSplitThreads) matmul_split_kernel(const __gri
 
   // every wait is bounded; whoever gives up tells the others
   auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-    if (abort_flag) return false;
-    if (mbar_wait_bounded(smem_addr(bar), parity, p.wait_limit_ns)) return true;
+    if (mbar_try_wait(smem_addr(bar), parity)) return true;
+    if (!abort_flag && mbar_wait_bounded(smem_addr(bar), parity, p.wait_limit_ns)) return true;
     abort_flag = 1;
     return false;
   };
@@ -331,10 +331,10 @@ __global__ void __launch_bounds__(kSplitThreads) matmul_split_kernel(const __gri
 // and sends 32 rows of them as one tensor-map store (or, for rows that tensor
 // maps cannot describe, element by element).
 constexpr int kPairThreads = 192;
-constexpr int kPairStages = 5;
+constexpr int kPairStages = 6;
 constexpr int kPairStageBytes = 32768;  // 128 tokens and 128 channels
 constexpr int kPairGroup = 8;
-constexpr int kPairSmem = kPairStages * kPairStageBytes + 4 * 2 * 4096 + 4 * 2048 + 1024;
+constexpr int kPairSmem = kPairStages * kPairStageBytes + 4 * 4096 + 4 * 2048 + 1024;
 
 __global__ void __launch_bounds__(kPairThreads) matmul_pair_kernel(const __grid_constant__ MatmulParams p) {
   namespace cg = cooperative_groups;
@@ -376,8 +376,8 @@ __global__ void __launch_bounds__(kPairThreads) matmul_pair_kernel(const __grid_
   // every wait is bounded; whoever gives up tells this CTA's others (the peer's
   // waits run out too)
   auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-    if (abort_flag) return false;
-    if (mbar_wait_bounded(smem_addr(bar), parity, p.wait_limit_ns)) return true;
+    if (mbar_try_wait(smem_addr(bar), parity)) return true;
+    if (!abort_flag && mbar_wait_bounded(smem_addr(bar), parity, p.wait_limit_ns)) return true;
     abort_flag = 1;
     return false;
   };
@@ -392,42 +392,51 @@ __global__ void __launch_bounds__(kPairThreads) matmul_pair_kernel(const __grid_
 
   if (warp == 0) {
     if (lane == 0) {
-      int64_t i = 0;  // stages filled so far
+      // stage s, its round's parity; both CTAs' copies complete on the first
+      // one's barrier
+      int s = 0, filled = 0;
+      uint32_t round = 0;
       bool ok = true;
+      const uint32_t full0 = peer_addr(smem_addr(&full[0]), 0);
       for (int64_t t = blockIdx.x >> 1; ok && t < tiles; t += pairs) {
         int64_t t0, c0;
         tile_at(t, &t0, &c0);
-        for (int kc = 0; kc < chunks; ++kc, ++i) {
-          const int s = static_cast<int>(i % kPairStages);
-          if (i >= kPairStages && !wait(&empty[s], (static_cast<uint32_t>(i / kPairStages) & 1) ^ 1)) {
+        const int tx = static_cast<int>(t0 + rank * 128), cw = static_cast<int>(c0 + rank * 128);
+        for (int kc = 0; kc < chunks; ++kc) {
+          if (filled == kPairStages && !wait(&empty[s], round ^ 1)) {
             ok = false;
             break;
           }
-          // both CTAs' copies complete on the first one's barrier
           if (rank == 0) mbar_arrive_expect_tx(smem_addr(&full[s]), 2 * kPairStageBytes);
-          const uint32_t bar = peer_addr(smem_addr(&full[s]), 0), at = base + s * kPairStageBytes;
-          tma_2d_pair(at, &p.map_x, kc * kTileK, static_cast<int>(t0 + rank * 128), bar);
-          tma_2d_pair(at + 16384, &p.map_w, kc * kTileK, static_cast<int>(c0 + rank * 128), bar);
+          const uint32_t bar = full0 + 8 * s, at = base + s * kPairStageBytes;
+          tma_2d_pair(at, &p.map_x, kc * kTileK, tx, bar);
+          tma_2d_pair(at + 16384, &p.map_w, kc * kTileK, cw, bar);
+          if (filled < kPairStages) ++filled;
+          if (++s == kPairStages) {
+            s = 0;
+            round ^= 1;
+          }
         }
       }
       if (abort_flag && rank == 0)  // copies still in flight must land before the pair ends
-        for (int64_t j = i > kPairStages ? i - kPairStages : 0; j < i; ++j)
-          mbar_wait_bounded(smem_addr(&full[j % kPairStages]), static_cast<uint32_t>(j / kPairStages) & 1,
-                            p.wait_limit_ns);
+        for (; filled > 0; --filled) {
+          if (s == 0) round ^= 1;
+          s = s == 0 ? kPairStages - 1 : s - 1;
+          mbar_wait_bounded(smem_addr(&full[s]), round, p.wait_limit_ns);
+        }
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       const uint32_t idesc = i8_instr_desc(256, 256);
-      int64_t i = 0;
-      int n_tile = 0;
+      int s = 0, n_tile = 0;
+      uint32_t round = 0;
       bool ok = true;
       for (int64_t t = blockIdx.x >> 1; ok && t < tiles; t += pairs, ++n_tile) {
         const int buf = n_tile & 1;
         if (n_tile >= 2 && !wait(&acc_empty[buf], ((n_tile >> 1) & 1) ^ 1)) break;
         tc_fence_after();
-        for (int kc = 0; kc < chunks; ++kc, ++i) {
-          const int s = static_cast<int>(i % kPairStages);
-          if (!wait(&full[s], static_cast<uint32_t>(i / kPairStages) & 1)) {
+        for (int kc = 0; kc < chunks; ++kc) {
+          if (!wait(&full[s], round)) {
             ok = false;
             break;
           }
@@ -438,6 +447,10 @@ __global__ void __launch_bounds__(kPairThreads) matmul_pair_kernel(const __grid_
           for (int j = 0; j < kTileK / kMmaK; ++j)
             mma_i8<2>(tmem + buf * 256, a + 2 * j, b + 2 * j, idesc, kc > 0 || j > 0);
           mma_commit_pair(smem_addr(&empty[s]));
+          if (++s == kPairStages) {
+            s = 0;
+            round ^= 1;
+          }
         }
         if (ok) mma_commit_pair(smem_addr(&acc_full[buf]));
       }
@@ -448,12 +461,12 @@ __global__ void __launch_bounds__(kPairThreads) matmul_pair_kernel(const __grid_
     }
   } else {
     const int quarter = warp & 3;
-    const uint32_t buffers = base + kPairStages * kPairStageBytes + (warp - 2) * 8192;
+    const uint32_t buffers = base + kPairStages * kPairStageBytes + (warp - 2) * 4096;
     float *sw = reinterpret_cast<float *>(dyn + (base - smem_addr(dyn)) + kPairStages * kPairStageBytes +
-                                          4 * 8192 + (warp - 2) * 2048);
+                                          4 * 4096 + (warp - 2) * 2048);
     float *bias = sw + 256;
     const int esz = p.out == 2 ? 4 : 2, cols = 128 / esz;  // columns of 128 bytes
-    int n_tile = 0, sent = 0;
+    int n_tile = 0;
     for (int64_t t = blockIdx.x >> 1; t < tiles; t += pairs, ++n_tile) {
       int64_t t0, c0;
       tile_at(t, &t0, &c0);
@@ -479,11 +492,11 @@ __global__ void __launch_bounds__(kPairThreads) matmul_pair_kernel(const __grid_
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(peer_addr(smem_addr(&acc_empty[buf]), 0));
         }
-        // a new 128-byte buffer: the store before last must have read it
-        const uint32_t at = buffers + (sent & 1) * 4096 + lane * 128;
+        // 128 more bytes of the rows: the last store must have read the buffer
+        const uint32_t at = buffers + lane * 128;
         const int chunk0 = (col % cols) * esz / 16;
         if (chunk0 == 0) {
-          if (lane == 0) bulk_wait_read<1>();
+          if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
         }
 #pragma unroll
@@ -517,12 +530,12 @@ __global__ void __launch_bounds__(kPairThreads) matmul_pair_kernel(const __grid_
           if (lane == 0) {
             if (c < p.n && first < p.m)
               tma_store_2d(&p.map_y, static_cast<int>(c), static_cast<int>(first),
-                           buffers + (sent & 1) * 4096);
+                           buffers);
             bulk_commit();  // (an empty group too: the waits count groups)
           }
         } else {
           __syncwarp();
-          const unsigned char *from = dyn + (buffers + (sent & 1) * 4096 - smem_addr(dyn));
+          const unsigned char *from = dyn + (buffers - smem_addr(dyn));
           for (int r2 = 0; r2 < 32 && first + r2 < p.m; ++r2)
             for (int j = lane; j < cols && c + j < p.n; j += 32) {
               const unsigned char *e = from + r2 * 128 + (((j * esz / 16) ^ (r2 & 7)) << 4) + (j * esz) % 16;
@@ -532,7 +545,6 @@ __global__ void __launch_bounds__(kPairThreads) matmul_pair_kernel(const __grid_
             }
           __syncwarp();
         }
-        ++sent;
       }
     }
     if (lane == 0) bulk_wait_all();
