@@ -186,7 +186,7 @@ class _Torch:
 
     def __init__(self):
         import torch
-        self.empty = torch.empty
+        self.empty_like, self.empty_strided = torch.empty_like, torch.empty_strided
         self.Tensor = torch.Tensor
         self.int8, self.uint8, self.int32 = torch.int8, torch.uint8, torch.int32
         self.float32, self.bfloat16 = torch.float32, torch.bfloat16
@@ -206,6 +206,13 @@ def _torch():
     if _torch_cache is None:
         _torch_cache = _Torch()
     return _torch_cache
+
+
+def _codes_of(T, shape, n, qdtype):
+    """(shape, dtype) of the codes of rows of n values in a tensor of `shape`."""
+    if qdtype == "int8":
+        return shape, T.int8
+    return _codes_like(tuple(shape[:-1]), n, qdtype)
 
 
 def _operand(t, name, device, dtype, shape=None):
@@ -237,6 +244,23 @@ def _on_stream(call, device, stream):
         raise ValueError(f"stream is on {stream.device}, not on {device}")
     with T.cuda.stream(stream):  # (the device too)
         return call(stream.cuda_stream)
+
+
+def _output(given, name, x, shape, dtype):
+    """An output and its address: the tensor given (checked), or a new one
+    beside x (by the cheapest of torch's ways to make it)."""
+    if given is not None:
+        return given, _operand(given, name, x.device, dtype, shape)
+    T = _torch()
+    if shape is x.shape or shape == x.shape:
+        t = T.empty_like(x, dtype=dtype)
+    elif len(shape) == 2:
+        t = T.empty_strided(shape, (shape[1], 1), dtype=dtype, device=x.device)
+    elif len(shape) == 1:
+        t = T.empty_strided(shape, (1,), dtype=dtype, device=x.device)
+    else:
+        t = x.new_empty(shape, dtype=dtype)
+    return t, t.data_ptr()
 
 
 _status_blocks = {}
@@ -283,12 +307,7 @@ def quant_matmul(x, scale_x, w, scale_w, bias=None, *, out_dtype=None, stream=No
     oshape = (*lead, n)
 
     def call(s):
-        y = out
-        if y is None:
-            y = T.empty(oshape, dtype=out_dtype, device=device)
-            py = y.data_ptr()
-        else:
-            py = _operand(y, "out", device, out_dtype, oshape)
+        y, py = _output(out, "out", x, oshape, out_dtype)
         st = _abi.lib().arnq_quant_matmul(
             x.data_ptr(), psx, pw, psw, pb, x.numel() // k if k else 0, n, k, code, py,
             _status_block(device, s), _abi.ARNQ_WORKSPACE_BYTES, s)
@@ -297,27 +316,6 @@ def quant_matmul(x, scale_x, w, scale_w, bias=None, *, out_dtype=None, stream=No
         return y
 
     return _on_stream(call, device, stream)
-
-
-def _outputs(given, specs, device):
-    """Tensors and addresses of a call's outputs: those given (checked) or new
-    ones.  specs: (name, shape, dtype), or None for one the call has not."""
-    T = _torch()
-    made, at = [], []
-    for spec in specs:
-        if spec is None:
-            made.append(None)
-            at.append(None)
-            continue
-        name, shape, dtype = spec
-        t = given.get(name) if given else None
-        if t is None:
-            t = T.empty(shape, dtype=dtype, device=device)
-            at.append(t.data_ptr())
-        else:
-            at.append(_operand(t, name, device, dtype, shape))
-        made.append(t)
-    return made, at
 
 
 def post_norm_add_rms_norm_dynamic_quant(h, x, gamma_post, gamma, beta=None, gate=None, smooth=None,
@@ -364,21 +362,24 @@ def post_norm_add_rms_norm_dynamic_quant(h, x, gamma_post, gamma, beta=None, gat
             raise ValueError(f"gate must have shape [{n}] or [g, {n}], got {tuple(gate.shape)}")
         gate_rows = gate.numel() // n if n else 0
     if qdtype is None:
-        q, specs = _abi.ARNQ_NO_CODES, [("y", shape, dt), None, ("x_out", shape, dt)]
+        q, cshape, cdt = _abi.ARNQ_NO_CODES, shape, dt
     else:
-        cshape, cdt = _codes_like(lead, n, qdtype)
-        q = _QDT[qdtype]
-        specs = [("y", cshape, cdt), ("scale", lead, T.float32), ("x_out", shape, dt)]
+        q, (cshape, cdt) = _QDT.get(qdtype), _codes_of(T, shape, n, qdtype)
+    given = out or {}
 
     def call(s):
-        made, at = _outputs(out, specs, device)
+        y, py = _output(given.get("y"), "y", x, cshape, cdt)
+        scale, psc = None, None
+        if qdtype is not None:
+            scale, psc = _output(given.get("scale"), "scale", x, lead, T.float32)
+        xo, pxo = _output(given.get("x_out"), "x_out", x, shape, dt)
         st = _abi.lib().arnq_post_norm_add_rms_norm_dynamic_quant(
             ph, x.data_ptr(), pgp, pgate, gate_rows, residual_scale, pg, pb, ps,
             x.numel() // n if n else 0, n, code, eps if eps_post is None else eps_post, eps, q,
-            at[0], at[1], at[2], s)
+            py, psc, pxo, s)
         if st != _abi.ARNQ_OK:
             raise ArnqError(st, "arnq_post_norm_add_rms_norm_dynamic_quant")
-        return tuple(made)
+        return y, scale, xo
 
     return _on_stream(call, device, stream)
 
@@ -407,16 +408,17 @@ def glu_dynamic_quant(x, smooth=None, *, activation: str = "silu", qdtype: str =
         raise ValueError(f"x must have an even last dimension (gate and up), got {tuple(shape)}")
     n, lead = shape[-1] // 2, shape[:-1]
     ps = None if smooth is None else _operand(smooth, "smooth", device, dt, (n,))
-    cshape, cdt = _codes_like(lead, n, qdtype)
-    specs = [("y", cshape, cdt), ("scale", lead, T.float32)]
+    cshape, cdt = _codes_of(T, (*lead, n), n, qdtype)
+    given = out or {}
 
     def call(s):
-        made, at = _outputs(out, specs, device)
+        y, py = _output(given.get("y"), "y", x, cshape, cdt)
+        scale, psc = _output(given.get("scale"), "scale", x, lead, T.float32)
         st = _abi.lib().arnq_glu_dynamic_quant(
-            x.data_ptr(), ps, x.numel() // (2 * n) if n else 0, n, code, act, _QDT[qdtype], at[0],
-            at[1], s)
+            x.data_ptr(), ps, x.numel() // (2 * n) if n else 0, n, code, act, _QDT[qdtype], py, psc,
+            s)
         if st != _abi.ARNQ_OK:
             raise ArnqError(st, "arnq_glu_dynamic_quant")
-        return tuple(made)
+        return y, scale
 
     return _on_stream(call, device, stream)

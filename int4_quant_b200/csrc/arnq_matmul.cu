@@ -60,22 +60,72 @@ bool encode_out(CUtensorMap *map, void *y, int64_t m, int64_t n, int out) {
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kStatic = 2048;  // the kernels' static shared memory, rounded up
 
-arnq_status launch_split(MatmulParams &p, bool plain, int sms, int dev, cudaStream_t stream) {
+// ---- the choice of kernel and split, by estimated time in us
+//
+// Fitted to a B200 (launches back to back, weights from HBM): a CTA of the
+// split kernel takes some 0.45 us a chunk of 128 codes of K alone on its SM and
+// 0.7 beside another, streams at 5.5 TB/s altogether, and has 3.5 us of fixed
+// cost plus 0.035 us a token of the tile for the exchange of partial sums; a
+// CTA pair 0.32 us a chunk and 8 us.  Measured, us, split / pair:
+//   n x k          m = 1        64           128          256          333
+//   4096 x 4096    6.7 / 17.5   9.7 / 17.7   12.8 / 18.1  18.6 / 18.2  19.2 / 18.6
+//   5120 x 7168    11.8 / 26.1  14.5 / 26.3  19.3 / 26.6  29.3 / 26.8  36.1 / 27.0
+//   16384 x 4096   16.3 / 23.5  19.5 / 20.1  23.1 / 20.6  34.0 / 21.0  53 / 31
+//   4096 x 16384   18.3 / 49.7  20.3 / 49.8  24.3 / 50.2  29.9 / 50.4  39.1 / 50.4
+struct SplitPlan {
+  int tokens, split, stages, per_sm;
+  double us;
+};
+
+double stream_us(const MatmulParams &p) {
+  return static_cast<double>(p.n * p.k + p.m * p.k) / 5.5e6;
+}
+
+SplitPlan plan_split(const MatmulParams &p, int sms) {
+  SplitPlan best = {};
   const int64_t token_tiles = div_up(p.m, 256);
-  p.tokens = static_cast<int32_t>(div_up(div_up(p.m, token_tiles), 16) * 16);
-  const int64_t tiles = div_up(p.n, 128);
+  const int tokens = static_cast<int>(div_up(div_up(p.m, token_tiles), 16) * 16);
+  const int64_t tiles = div_up(p.n, 128) * token_tiles;
   const int chunks = static_cast<int>(div_up(p.k, kTileK));
-  // CTAs for every SM: K shared out while that leaves SMs idle, two chunks each at least
-  int split = 1;
-  while (split < 8 && tiles * token_tiles * split * 2 <= sms && chunks >= 4 * split) split *= 2;
+  const int stage = 16384 + tokens * 128;
+  for (int split = 1; split <= 8 && (split == 1 || chunks >= 2 * split); split *= 2) {
+    const int mine = static_cast<int>(div_up(chunks, split));
+    // two CTAs an SM where at least three stages (or all there are) fit half of it
+    int stages = (kSmemLimit / 2 - kStatic - 1024) / stage, per_sm = 2;
+    if (stages < 3 && stages < mine) {
+      stages = (kSmemLimit - kStatic - 1024) / stage;
+      per_sm = 1;
+    }
+    if (tokens * 512 > kSmemLimit / 2 - kStatic - 1024) per_sm = 1;
+    if (stages > kSplitMaxStages) stages = kSplitMaxStages;
+    if (stages > mine) stages = mine;
+    const int64_t ctas = tiles * split;
+    const double rounds = static_cast<double>(div_up(ctas, static_cast<int64_t>(per_sm) * sms));
+    const double beside = per_sm == 2 && ctas > sms ? 1.5 : 1.0;
+    double us = rounds * mine * 0.45 * beside;
+    if (us < stream_us(p)) us = stream_us(p);
+    us += 3.5 + (split > 1 ? 0.035 : 0.02) * tokens * rounds;
+    if (best.split == 0 || us < best.us) best = SplitPlan{tokens, split, stages, per_sm, us};
+  }
+  return best;
+}
+
+double pair_us(const MatmulParams &p, int pairs) {
+  const int64_t tiles = div_up(p.m, 256) * div_up(p.n, 256);
+  const double us = 0.32 * static_cast<double>(div_up(p.k, kTileK)) *
+                    static_cast<double>(div_up(tiles, static_cast<int64_t>(pairs)));
+  return 8.0 + (us < stream_us(p) ? stream_us(p) : us);
+}
+
+arnq_status launch_split(MatmulParams &p, const SplitPlan &plan, bool plain, int dev, cudaStream_t stream) {
+  const int64_t token_tiles = div_up(p.m, 256), tiles = div_up(p.n, 128);
+  const int split = plan.split;
+  p.tokens = plan.tokens;
   p.split = split;
+  p.stages = plan.stages;
   p.channel_tiles = static_cast<int32_t>(tiles);
   if (tiles * token_tiles * split > INT32_MAX) return ARNQ_ERR_SHAPE;
-  const int stage = 16384 + p.tokens * 128;
-  int stages = (kSmemLimit - kStatic - 1024) / stage;
-  if (stages > kSplitMaxStages) stages = kSplitMaxStages;
-  p.stages = stages;
-  int smem = stages * stage;
+  int smem = p.stages * (16384 + p.tokens * 128);
   if (smem < p.tokens * 512) smem = p.tokens * 512;  // the partial sums lie over the stages
   smem += 1024;
   p.tmem_cols = 32;
@@ -85,13 +135,14 @@ arnq_status launch_split(MatmulParams &p, bool plain, int sms, int dev, cudaStre
   const void *fn = plain ? reinterpret_cast<const void *>(matmul_split_kernel<true>)
                          : reinterpret_cast<const void *>(matmul_split_kernel<false>);
   int per_sm = 0;
-  const arnq_status st = resident_ctas(fn, dev, kSplitThreads, smem, &per_sm);
+  // (raises the shared-memory limit)
+  const arnq_status st = resident_ctas(fn, dev, plain ? kPlainThreads : kSplitThreads, smem, &per_sm);
   if (st != ARNQ_OK) return st;
-  return launch_dependent(fn, dim3(static_cast<unsigned>(tiles * token_tiles * split)), kSplitThreads,
-                          smem, split, stream, &p);
+  return launch_dependent(fn, dim3(static_cast<unsigned>(tiles * token_tiles * split)),
+                          plain ? kPlainThreads : kSplitThreads, smem, split, stream, &p);
 }
 
-arnq_status launch_pair(MatmulParams &p, int dev, cudaStream_t stream) {
+arnq_status launch_pair(MatmulParams &p, int pairs, cudaStream_t stream) {
   p.token_tiles = static_cast<int32_t>(div_up(p.m, 256));
   p.channel_tiles = static_cast<int32_t>(div_up(p.n, 256));
   const int esz = p.out == ARNQ_FP32 ? 4 : 2;
@@ -99,13 +150,10 @@ arnq_status launch_pair(MatmulParams &p, int dev, cudaStream_t stream) {
   if (!encode(&p.map_w, p.w, p.n, p.k, 128) || !encode(&p.map_x, p.x, p.m, p.k, 128) ||
       (p.tma_out && !encode_out(&p.map_y, p.y, p.m, p.n, p.out)))
     return ARNQ_ERR_CUDA;
-  const void *fn = reinterpret_cast<const void *>(matmul_pair_kernel);
-  int pairs = 0;
-  const arnq_status st = resident_clusters(fn, dev, kPairThreads, kPairSmem, 2, &pairs);
-  if (st != ARNQ_OK) return st;
   const int64_t tiles = static_cast<int64_t>(p.token_tiles) * p.channel_tiles;
   if (tiles < pairs) pairs = static_cast<int>(tiles);
-  return launch_dependent(fn, dim3(2 * pairs), kPairThreads, kPairSmem, 2, stream, &p);
+  return launch_dependent(reinterpret_cast<const void *>(matmul_pair_kernel), dim3(2 * pairs), kPairThreads,
+                          kPairSmem, 2, stream, &p);
 }
 
 }  // namespace
@@ -142,6 +190,14 @@ extern "C" arnq_status arnq_quant_matmul(const void *x, const float *scale_x, co
   p.vec_out = n % 4 == 0 && is_aligned(y, 4 * esz) ? 1 : 0;
   p.wait_limit_ns = kWaitLimitNs;
   const bool plain = k % 16 != 0 || !is_aligned(x, 16) || !is_aligned(w, 16);
-  if (!plain && m > 512) return launch_pair(p, dev, static_cast<cudaStream_t>(stream));
-  return launch_split(p, plain, sms, dev, static_cast<cudaStream_t>(stream));
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const SplitPlan plan = plan_split(p, sms);
+  if (!plain) {
+    int pairs = 0;
+    st = resident_clusters(reinterpret_cast<const void *>(matmul_pair_kernel), dev, kPairThreads, kPairSmem, 2,
+                           &pairs);
+    if (st != ARNQ_OK) return st;
+    if (pair_us(p, pairs) < plan.us) return launch_pair(p, pairs, cs);
+  }
+  return launch_split(p, plan, plain, dev, cs);
 }

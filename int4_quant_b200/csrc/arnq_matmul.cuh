@@ -86,6 +86,11 @@ __device__ __forceinline__ uint4 load16_any(const int8_t *base, int64_t at, int 
   const uintptr_t lo = reinterpret_cast<uintptr_t>(base);
   const uintptr_t hi = lo + static_cast<uintptr_t>(end);
   uint32_t w[5];
+  if (first >= lo && first + 20 <= hi) {
+    const uint32_t *q = reinterpret_cast<const uint32_t *>(first);
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = q[i];
+  } else {
 #pragma unroll
   for (int i = 0; i < 5; ++i) {
     const uintptr_t q = first + 4 * i;
@@ -100,6 +105,7 @@ __device__ __forceinline__ uint4 load16_any(const int8_t *base, int64_t at, int 
     }
     w[i] = v;
   }
+  }
   const uint32_t sh = static_cast<uint32_t>(a & 3) * 8;
   uint32_t r[4];
 #pragma unroll
@@ -111,19 +117,28 @@ __device__ __forceinline__ uint4 load16_any(const int8_t *base, int64_t at, int 
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// A tile of `rows` rows of 128 codes into swizzled shared memory, by `nt` threads.
+// A tile of `rows` rows of 128 codes into swizzled shared memory, by `nt`
+// threads, four 16-byte pieces of each in flight.
 __device__ __forceinline__ void load_tile_any(uint32_t dst, const int8_t *base, int64_t row0, int rows,
                                               int64_t all_rows, int64_t k, int64_t k0, int tid, int nt) {
-  for (int i = tid; i < rows * 8; i += nt) {
-    const int r = i >> 3, c = i & 7;
-    const int64_t at_k = k0 + c * 16, row = row0 + r;
-    const int64_t left = row < all_rows ? k - at_k : 0;
-    const int valid = left >= 16 ? 16 : static_cast<int>(left);
-    const uint4 v = load16_any(base, row * k + at_k, valid, all_rows * k);
-    const uint32_t addr = dst + r * 128 + ((c ^ (r & 7)) << 4);
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
-                 "r"(v.w)
-                 : "memory");
+  for (int i0 = tid; i0 < rows * 8; i0 += 4 * nt) {
+    uint4 v[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int i = i0 + g * nt;
+      const int64_t at_k = k0 + (i & 7) * 16, row = row0 + (i >> 3);
+      const int64_t left = i < rows * 8 && row < all_rows ? k - at_k : 0;
+      v[g] = load16_any(base, row * k + at_k, left >= 16 ? 16 : static_cast<int>(left), all_rows * k);
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int i = i0 + g * nt, r = i >> 3;
+      if (i >= rows * 8) break;
+      const uint32_t addr = dst + r * 128 + (((i & 7) ^ (r & 7)) << 4);
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[g].x), "r"(v[g].y),
+                   "r"(v[g].z), "r"(v[g].w)
+                   : "memory");
+    }
   }
 }
 
@@ -134,14 +149,15 @@ __device__ __forceinline__ void load_tile_any(uint32_t dst, const int8_t *base, 
 // CTAs.  Each CTA streams its part of the weights once; the partial sums meet
 // through distributed shared memory, added as integers (any order, same
 // result), each CTA finishing every split-th token.
-// Warps: 0 copies, 1 MMA and TMEM, 2-5 the epilogue (and, with PLAIN, the
-// loads, for codes that tensor maps cannot describe: k or the pointers not
-// multiples of 16).
-constexpr int kSplitThreads = 192;
+// Warps: 0 copies, 1 MMA and TMEM, 2-5 the epilogue.  With PLAIN, for codes
+// that tensor maps cannot describe (k or the pointers not multiples of 16),
+// warps 2-9 load.
+constexpr int kSplitThreads = 192, kPlainThreads = 320;
 constexpr int kSplitMaxStages = 12;
 
 template <bool PLAIN>
-__global__ void __launch_bounds__(kSplitThreads) matmul_split_kernel(const __grid_constant__ MatmulParams p) {
+__global__ void __launch_bounds__(PLAIN ? kPlainThreads : kSplitThreads)
+    matmul_split_kernel(const __grid_constant__ MatmulParams p) {
   namespace cg = cooperative_groups;
   extern __shared__ unsigned char dyn[];
   __shared__ __align__(8) uint64_t full[kSplitMaxStages], empty[kSplitMaxStages], done;
@@ -163,7 +179,7 @@ __global__ void __launch_bounds__(kSplitThreads) matmul_split_kernel(const __gri
 
   if (tid == 0) {
     for (int s = 0; s < stages; ++s) {
-      mbar_init(smem_addr(&full[s]), PLAIN ? 128 : 1);
+      mbar_init(smem_addr(&full[s]), PLAIN ? kPlainThreads - 64 : 1);
       mbar_init(smem_addr(&empty[s]), 1);
     }
     mbar_init(smem_addr(&done), 1);
@@ -191,7 +207,11 @@ __global__ void __launch_bounds__(kSplitThreads) matmul_split_kernel(const __gri
     sw[j] = j < have ? p.scale_w[c + j] : 0.f;
     b[j] = j < have ? load_bias(p, c + j) : 0.f;
   }
-  for (int t = tid - 64; t >= 0 && t < count; t += 128) sx[t] = p.scale_x[t0 + t];
+  for (int t = tid; t < count; t += blockDim.x) sx[t] = p.scale_x[t0 + t];
+
+  // The next kernel on the stream may become resident beside this one (it waits
+  // for this grid's completion before touching memory).
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // every wait is bounded; whoever gives up tells the others
   auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
@@ -241,8 +261,10 @@ __global__ void __launch_bounds__(kSplitThreads) matmul_split_kernel(const __gri
       const int s = i % stages;
       if (i >= stages && !wait(&empty[s], ((i / stages) & 1) ^ 1)) break;
       const uint32_t at = base + s * stage_bytes;
-      load_tile_any(at, p.w, c0, 128, p.n, p.k, static_cast<int64_t>(kc) * kTileK, lt, 128);
-      load_tile_any(at + 16384u, p.x, t0, p.tokens, p.m, p.k, static_cast<int64_t>(kc) * kTileK, lt, 128);
+      load_tile_any(at, p.w, c0, 128, p.n, p.k, static_cast<int64_t>(kc) * kTileK, lt,
+                    kPlainThreads - 64);
+      load_tile_any(at + 16384u, p.x, t0, p.tokens, p.m, p.k, static_cast<int64_t>(kc) * kTileK, lt,
+                    kPlainThreads - 64);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(smem_addr(&full[s]));
     }
@@ -251,7 +273,7 @@ __global__ void __launch_bounds__(kSplitThreads) matmul_split_kernel(const __gri
 
   // ---- partial sums to shared memory: part[t][channel], over the stages
   int32_t *part = reinterpret_cast<int32_t *>(base_ptr);
-  if (warp >= 2) {
+  if (warp >= 2 && warp < 6) {
     const bool ok = wait(&done, 0);
     tc_fence_after();
     const int quarter = warp & 3;
@@ -279,7 +301,7 @@ __global__ void __launch_bounds__(kSplitThreads) matmul_split_kernel(const __gri
   // ---- sums over the cluster, scales, output: a warp a token, four channels a
   // lane, four tokens at a time
   if (!failed && have > 0) {
-    constexpr int kStep = kSplitThreads / 32;
+    constexpr int kStep = (PLAIN ? kPlainThreads : kSplitThreads) / 32;
     for (int t = rank + warp * split; t < count; t += 4 * split * kStep) {
       int4 sum[4];
 #pragma unroll
@@ -311,7 +333,6 @@ __global__ void __launch_bounds__(kSplitThreads) matmul_split_kernel(const __gri
     }
   }
   cluster.sync();  // nobody leaves while its partial sums are being read
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ------------------------------------------------------------ many tokens

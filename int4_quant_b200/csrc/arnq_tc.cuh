@@ -90,26 +90,28 @@ __host__ __device__ constexpr uint32_t i8_instr_desc(int m, int n) {
 
 // ---- tcgen05 (CG: CTAs of the group that shares one instruction, 1 or 2)
 
+// Allocates `cols` TMEM columns (one warp) and gives up the right to allocate
+// more: while a CTA holds it, another one on the SM waits for its own.
 template <int CG>
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_slot, uint32_t cols) {
-  if (CG == 1)
+  if (CG == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_slot),
                  "r"(cols)
                  : "memory");
-  else
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  } else {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_slot),
                  "r"(cols)
                  : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
 }
 template <int CG>
 __device__ __forceinline__ void tmem_release(uint32_t taddr, uint32_t cols) {
-  if (CG == 1) {
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  if (CG == 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols));
-  } else {
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  else
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols));
-  }
 }
 // D[tmem] (+)= A[smem] * B[smem], one instruction of kMmaK codes
 template <int CG>
