@@ -2,6 +2,7 @@
 // choice between the kernels, launch.
 #include "arnq_matmul.cuh"
 
+#include <cmath>
 #include <cstring>
 
 #include "arnq_host.h"
@@ -64,7 +65,7 @@ constexpr int kStatic = 2048;  // the kernels' static shared memory, rounded up
 //
 // Fitted to a B200 (launches back to back, weights from HBM): a CTA of the
 // split kernel takes some 0.45 us a chunk of 128 codes of K alone on its SM and
-// 0.7 beside another, streams at 5.5 TB/s altogether, and has 3.5 us of fixed
+// 0.7 beside another (with plain loads 0.005 us a row of the chunk), streams at 5.5 TB/s altogether, and has 3.5 us of fixed
 // cost plus 0.035 us a token of the tile for the exchange of partial sums; a
 // CTA pair 0.32 us a chunk and 8 us.  Measured, us, split / pair:
 //   n x k          m = 1        64           128          256          333
@@ -81,31 +82,42 @@ double stream_us(const MatmulParams &p) {
   return static_cast<double>(p.n * p.k + p.m * p.k) / 5.5e6;
 }
 
-SplitPlan plan_split(const MatmulParams &p, int sms) {
+// CTAs resident at once in clusters of `split` (cudaOccupancyMaxActiveClusters:
+// 148, 148, 132, 120 at one CTA an SM, 296, 296, 284, 264 at two)
+double split_slots(int split, int per_sm, int sms) {
+  const double part = split <= 2 ? 1.0 : split == 4 ? (per_sm == 1 ? 0.89 : 0.95) : (per_sm == 1 ? 0.81 : 0.89);
+  return part * per_sm * sms;
+}
+
+SplitPlan plan_split(const MatmulParams &p, bool plain, int sms) {
   SplitPlan best = {};
-  const int64_t token_tiles = div_up(p.m, 256);
-  const int tokens = static_cast<int>(div_up(div_up(p.m, token_tiles), 16) * 16);
-  const int64_t tiles = div_up(p.n, 128) * token_tiles;
   const int chunks = static_cast<int>(div_up(p.k, kTileK));
-  const int stage = 16384 + tokens * 128;
-  for (int split = 1; split <= 8 && (split == 1 || chunks >= 2 * split); split *= 2) {
-    const int mine = static_cast<int>(div_up(chunks, split));
-    // two CTAs an SM where at least three stages (or all there are) fit half of it
-    int stages = (kSmemLimit / 2 - kStatic - 1024) / stage, per_sm = 2;
-    if (stages < 3 && stages < mine) {
-      stages = (kSmemLimit - kStatic - 1024) / stage;
-      per_sm = 1;
+  const int64_t least = div_up(p.m, 256);  // token tiles; more of them spread a small product
+  for (int64_t token_tiles = least; token_tiles <= 4 * least; token_tiles *= 2) {
+    const int tokens = static_cast<int>(div_up(div_up(p.m, token_tiles), 16) * 16);
+    if (token_tiles > least && tokens < 32) break;
+    const int64_t tiles = div_up(p.n, 128) * div_up(p.m, tokens);
+    const int stage = 16384 + tokens * 128;
+    for (int split = 1; split <= 8 && (split == 1 || chunks >= (plain ? 1 : 2) * split); split *= 2) {
+      const int mine = static_cast<int>(div_up(chunks, split));
+      // two CTAs an SM where at least three stages (or all there are) fit half of it
+      int stages = (kSmemLimit / 2 - kStatic - 1024) / stage, per_sm = 2;
+      if (stages < 3 && stages < mine) {
+        stages = (kSmemLimit - kStatic - 1024) / stage;
+        per_sm = 1;
+      }
+      if (tokens * 512 > kSmemLimit / 2 - kStatic - 1024) per_sm = 1;
+      if (stages > kSplitMaxStages) stages = kSplitMaxStages;
+      if (stages > mine) stages = mine;
+      const int64_t ctas = tiles * split;
+      const double rounds = std::ceil(static_cast<double>(ctas) / split_slots(split, per_sm, sms));
+      const double beside = per_sm == 2 && ctas > sms ? 1.5 : 1.0;
+      const double chunk_us = plain ? 0.005 * (128 + tokens) : 0.45;
+      double us = rounds * mine * chunk_us * beside;
+      if (us < stream_us(p)) us = stream_us(p);
+      us += 3.5 + (split > 1 ? 0.035 : 0.02) * tokens * rounds;
+      if (best.split == 0 || us < best.us) best = SplitPlan{tokens, split, stages, per_sm, us};
     }
-    if (tokens * 512 > kSmemLimit / 2 - kStatic - 1024) per_sm = 1;
-    if (stages > kSplitMaxStages) stages = kSplitMaxStages;
-    if (stages > mine) stages = mine;
-    const int64_t ctas = tiles * split;
-    const double rounds = static_cast<double>(div_up(ctas, static_cast<int64_t>(per_sm) * sms));
-    const double beside = per_sm == 2 && ctas > sms ? 1.5 : 1.0;
-    double us = rounds * mine * 0.45 * beside;
-    if (us < stream_us(p)) us = stream_us(p);
-    us += 3.5 + (split > 1 ? 0.035 : 0.02) * tokens * rounds;
-    if (best.split == 0 || us < best.us) best = SplitPlan{tokens, split, stages, per_sm, us};
   }
   return best;
 }
@@ -118,7 +130,7 @@ double pair_us(const MatmulParams &p, int pairs) {
 }
 
 arnq_status launch_split(MatmulParams &p, const SplitPlan &plan, bool plain, int dev, cudaStream_t stream) {
-  const int64_t token_tiles = div_up(p.m, 256), tiles = div_up(p.n, 128);
+  const int64_t token_tiles = div_up(p.m, plan.tokens), tiles = div_up(p.n, 128);
   const int split = plan.split;
   p.tokens = plan.tokens;
   p.split = split;
@@ -191,7 +203,7 @@ extern "C" arnq_status arnq_quant_matmul(const void *x, const float *scale_x, co
   p.wait_limit_ns = kWaitLimitNs;
   const bool plain = k % 16 != 0 || !is_aligned(x, 16) || !is_aligned(w, 16);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const SplitPlan plan = plan_split(p, sms);
+  const SplitPlan plan = plan_split(p, plain, sms);
   if (!plain) {
     int pairs = 0;
     st = resident_clusters(reinterpret_cast<const void *>(matmul_pair_kernel), dev, kPairThreads, kPairSmem, 2,
