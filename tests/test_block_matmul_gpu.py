@@ -223,3 +223,11 @@ def test_many_tokens_leaves_neighbours_alone():
     lib.quant_matmul(x, sx, w, sw, out=buf[:777])
     check(x, sx, w, sw, None, buf[:777])
     assert (buf[777:] == 7).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(8192, 7168, 256), (4500, 2560, 384), (2816, 6000, 128), (9000, 4352, 1040),
+                                   (40000, 520, 512)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_more_tiles_than_pairs(m, n, k, out):
+    # several tiles for each pair of CTAs: two at a time, singles behind them, odd rows of tiles
+    run(m, n, k, out, out == torch.float32, seed=m)
