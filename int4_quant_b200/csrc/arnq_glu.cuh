@@ -68,13 +68,13 @@ __device__ __noinline__ double glu64(const uint16_t *gate, const uint16_t *up, c
   return smooth ? in * static_cast<double>(Cvt<T>::f1(*smooth)) : in;
 }
 
-template <class T_, int ACT, int QT_, bool VEC_, int UPT_>
+template <class T_, int ACT, int QT_, bool VEC_, int UPT_, bool FULL_ = false>
 struct GluOp {
   typedef T_ T;
   typedef GluParams Params;
   static constexpr int QT = QT_, UPT = UPT_, kInputs = 2;
   static constexpr bool kReadsSlots = true;
-  static constexpr bool VEC = VEC_, STAGED = VEC_ && UPT_ > 0;
+  static constexpr bool FULL = FULL_, VEC = VEC_, STAGED = VEC_ && UPT_ > 0;
   static constexpr int kMaxThreads = UPT == 4 ? 512 : 1024, kMinCtas = UPT == 4 ? 2 : 1;
   struct Keep {
     float low;  // the unit's smallest z, at most 0

@@ -8,6 +8,13 @@ using namespace arnq;
 
 template <class T, int QT, bool VEC>
 arnq_status by_upt(const NormsParams &p, int upt, int threads, cudaStream_t s) {
+  if constexpr (VEC) {
+    if (p.out.units == upt * threads) {
+      if (upt == 1) return launch_rows<NormsOp<T, QT, VEC, 1, true>>(p, threads, s);
+      if (upt == 2) return launch_rows<NormsOp<T, QT, VEC, 2, true>>(p, threads, s);
+      if (upt == 4) return launch_rows<NormsOp<T, QT, VEC, 4, true>>(p, threads, s);
+    }
+  }
   if (upt == 1) return launch_rows<NormsOp<T, QT, VEC, 1>>(p, threads, s);
   if (upt == 2) return launch_rows<NormsOp<T, QT, VEC, 2>>(p, threads, s);
   if (upt == 4) return launch_rows<NormsOp<T, QT, VEC, 4>>(p, threads, s);

@@ -97,16 +97,16 @@ __device__ __noinline__ double sumsq_cold(const uint16_t *a, const uint16_t *h, 
   return s;
 }
 
-template <class T_, int QT_, bool VEC_, int UPT_>
+template <class T_, int QT_, bool VEC_, int UPT_, bool FULL_ = false>
 struct NormsOp {
   typedef T_ T;
   typedef NormsParams Params;
   static constexpr int QT = QT_, UPT = UPT_, kInputs = 2;
   static constexpr bool kReadsSlots = false;  // after prepare()
-  static constexpr bool VEC = VEC_, STAGED = VEC_ && UPT_ > 0;
+  static constexpr bool FULL = FULL_, VEC = VEC_, STAGED = VEC_ && UPT_ > 0;
   static constexpr int kMaxThreads = UPT == 4 ? 384 : 1024, kMinCtas = UPT == 4 ? 2 : 1;
   struct Keep {
-    uint4 x;  // x' of the unit
+    float2 f[4];  // the unit's h, then its x'
   };
   // Error of v = x + (h G) f in units of 2^-24: the factor f one of |h G f|, the
   // product h G none in bf16 (8 + 16 bits) and one in fp16 (11 + 22), the
@@ -151,14 +151,19 @@ struct NormsOp {
     return STAGED ? slot[stride] : load_unit<VEC, false>(p.x + row * p.out.n, u, p.out.n);
   }
   // long rows: x' of a unit after the row's first phases, read back or made again
-  __device__ __forceinline__ uint4 x_again(int64_t row, int u) const {
-    if (p.x_out) return load_unit<VEC, false>(p.x_out + row * p.out.n, u, p.out.n);
-    return make_x(row, u, get_h(row, u, nullptr), get_x(row, u, nullptr, 0));
+  __device__ __forceinline__ void x_again(int64_t row, int u, Keep &keep) const {
+    if (p.x_out) {
+      unpack<T>(load_unit<VEC, false>(p.x_out + row * p.out.n, u, p.out.n), keep.f);
+    } else {
+      unpack<T>(get_h(row, u, nullptr), keep.f);
+      make_x(row, u, keep, nullptr, 0);
+    }
   }
 
-  __device__ __forceinline__ uint4 make_x(int64_t row, int u, const uint4 &hw, const uint4 &xw) const {
-    float2 h[4], x[4], G[4];
-    unpack<T>(hw, h);
+  // keep: the unit's h, turned into its x', which is returned packed too
+  __device__ __forceinline__ uint4 make_x(int64_t row, int u, Keep &keep, const uint4 *slot, int stride) const {
+    float2 x[4], G[4];
+    const uint4 xw = get_x(row, u, slot, stride);
     unpack<T>(xw, x);
     unpack<T>(load_unit<VEC, false>(p.gamma_post, u, p.out.n), G);
     times(G, gate_row, u);
@@ -167,7 +172,7 @@ struct NormsOp {
     float tmax = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float2 hg = __fmul2_rn(h[k], G[k]);
+      const float2 hg = __fmul2_rn(keep.f[k], G[k]);
       v[k] = __ffma2_rn(hg, f, x[k]);
       tmax = abs_max3(hg.x, hg.y, tmax);
     }
@@ -186,8 +191,9 @@ struct NormsOp {
     }
     uint4 r = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     if (differ)
-      r = settle_x<T>(r, make_uint4(hi[0], hi[1], hi[2], hi[3]), hw, xw, p.gamma_post + 8 * u,
+      r = settle_x<T>(r, make_uint4(hi[0], hi[1], hi[2], hi[3]), get_h(row, u, slot), xw, p.gamma_post + 8 * u,
                       gate_row ? gate_row + 8 * u : nullptr, post.inv64, p.out.n - 8 * u);
+    unpack<T>(r, keep.f);
     return r;
   }
 
@@ -201,7 +207,10 @@ struct NormsOp {
                       : nullptr;
     // ---- Rms of h
     double ss = 0.0;
-    each([&](int u, int i) { ss += sumsq<T>(get_h(row, u, slot + i * nt)); });
+    each([&](int u, int i) {
+      unpack<T>(get_h(row, u, slot + i * nt), keep[i].f);
+      ss += sumsq(keep[i].f);
+    });
     ss = block_sum(ss, sm.sum[0], nwarps);
     bool cold = ss_out_of_range(ss, p.eps_post);
     if (cold) {  // the same for every thread
@@ -212,9 +221,10 @@ struct NormsOp {
     // ---- x' and its Rms
     ss = 0.0;
     each([&](int u, int i) {
-      keep[i].x = make_x(row, u, get_h(row, u, slot + i * nt), get_x(row, u, slot + i * nt, stride));
-      ss += sumsq<T>(keep[i].x);
-      if (p.x_out) store_unit<VEC>(p.x_out + row * p.out.n, u, p.out.n, keep[i].x);
+      if (UPT == 0) unpack<T>(get_h(row, u, nullptr), keep[0].f);
+      const uint4 x = make_x(row, u, keep[i], slot + i * nt, stride);
+      ss += sumsq(keep[i].f);
+      if (p.x_out) store_unit<VEC>(p.x_out + row * p.out.n, u, p.out.n, x);
     });
     ss = block_sum(ss, sm.sum[1], nwarps);
     cold = ss_out_of_range(ss, p.eps);
@@ -228,9 +238,8 @@ struct NormsOp {
   }
 
   __device__ __forceinline__ bool value(int64_t row, int u, Keep &keep, const uint4 *, int, float2 v[4]) const {
-    if (UPT == 0) keep.x = x_again(row, u);
-    float2 x[4], G[4], B[4];
-    unpack<T>(keep.x, x);
+    if (UPT == 0) x_again(row, u, keep);
+    float2 G[4], B[4];
     unpack<T>(load_unit<VEC, false>(p.gamma, u, p.out.n), G);
     times(G, p.smooth, u);
     const float2 r = make_float2(pre.inv, pre.inv);
@@ -238,10 +247,10 @@ struct NormsOp {
       unpack<T>(load_unit<VEC, false>(p.beta, u, p.out.n), B);
       times(B, p.smooth, u);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = __ffma2_rn(__fmul2_rn(x[k], r), G[k], B[k]);
+      for (int k = 0; k < 4; ++k) v[k] = __ffma2_rn(__fmul2_rn(keep.f[k], r), G[k], B[k]);
     } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = __fmul2_rn(__fmul2_rn(x[k], r), G[k]);
+      for (int k = 0; k < 4; ++k) v[k] = __fmul2_rn(__fmul2_rn(keep.f[k], r), G[k]);
     }
     return !pre.cold;
   }

@@ -99,10 +99,7 @@ __device__ __forceinline__ uint16_t round16(double v) {
 // Sum of squares of a unit in fp64.  Each square is exact in binary32 (but for
 // overflow and underflow), which is cheaper than squaring in fp64; adding
 // them in binary32, even four at a time, was seen to move a rounding of x'.
-template <class T>
-__device__ __forceinline__ double sumsq(const uint4 &w) {
-  float2 f[4];
-  unpack<T>(w, f);
+__device__ __forceinline__ double sumsq(const float2 f[4]) {
   double s = 0.0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -239,8 +236,9 @@ __device__ __forceinline__ void flagged_units(const Op &op, int64_t row, unsigne
 
 // Op: struct with
 //   Params, T, VEC (16-byte units), UPT (units per thread held in registers;
-//   0: rows longer than that are read again in every phase), QT (code type:
-//   0 INT8, 1 INT4, kQNone), STAGED (inputs staged as above), kInputs
+//   0: rows longer than that are read again in every phase), FULL (units fill
+//   the threads exactly: no unit is checked, which lets a thread's units
+//   overlap), QT (code type: 0 INT8, 1 INT4, kQNone), STAGED (inputs staged as above), kInputs
 //   (tensors staged), Keep (what a unit keeps besides its values)
 //   stage(row, u, slot, stride)     issues the copies of a unit
 //   prepare(...)                    the row's statistics
@@ -273,7 +271,7 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
         const int u = tid + i * nt;
-        if (u < units) f(u, i);
+        if (Op::FULL || u < units) f(u, i);
       }
     } else {
       for (int u = tid; u < units; u += nt) f(u, 0);
@@ -287,7 +285,7 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
         const int u = tid + i * nt;
-        if (u < units && f(u, i)) flags |= 1u << i;
+        if ((Op::FULL || u < units) && f(u, i)) flags |= 1u << i;
       }
       __syncwarp();
       if (__any_sync(0xFFFFFFFFu, flags != 0u)) flagged_units<NU>(op, row, flags, tid, nt, n, at, use);
