@@ -5,16 +5,17 @@
 //            z = 2 sqrt(2/pi) (g + 0.044715 g^3)   (GELU, tanh form: 0.5 (1 + tanh(z/2)) is the sigmoid of z)
 //   scale = row_max(|in|) / Q,  code = round(in / scale)
 //
-// Binary32 error of a value, in units of |in| 2^-24: the exponential's
-// argument is off by at most 6 |z| (roundings of z and of the product with
-// log2 e, the constants'), which the sigmoid passes on for z < 0 and weakens
-// to at most 0.28 * 6 for z > 0; the exponential (4), the division (4) and
-// the remaining roundings (3) add 11.  The quotient by the scale adds 3.
-// Altogether |error| <= |in| 2^-24 (20 + 8 max(-z, 0)) with a margin, for
-// z >= kLow.  Below that, where the sigmoid nears the end of binary32's range,
-// a value is at most 1.5e-33 |u smooth|: with |u smooth| <= 1e8 it and its
-// error are far below what a row's maximum of at least kTiny (1e-18) can tell
-// from zero; a row with a larger factor there is computed in fp64.
+// Binary32 error of a value, in units of |in| 2^-24: the exponential's argument
+// is off by at most 1.5 |z| (the product with log2 e and that constant's
+// rounding), for GELU 6 |z| (those of z too), which the sigmoid passes on for
+// z < 0 and weakens to at most 0.28 of it for z > 0; the exponential's own 4
+// (2 ulp), that for the reciprocal 2 and the three roundings of 1 + e and the
+// products add 9.  Altogether 9 + s max(-z, 0), s = 2 or 6, with a margin of one
+// for z > 0, for z >= kLow.  Below that, where the sigmoid nears the end of
+// binary32's range, a value is at most 1.5e-33 |u smooth|: with |u smooth| <=
+// 1e8 it and its error are far below what a row's maximum of at least kTiny
+// (1e-18) can tell from zero; a row with a larger factor there is computed in
+// fp64.
 #pragma once
 
 #include "arnq_rowquant.cuh"
@@ -105,11 +106,6 @@ struct GluOp {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));
     return e;
   }
-  static __device__ __forceinline__ float rcp_approx(float y) {
-    float e;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));
-    return e;
-  }
   __device__ __forceinline__ bool value(int64_t row, int u, Keep &keep, const uint4 *slot, int stride,
                                         float2 v[4]) const {
     float2 g[4], t[4];
@@ -142,19 +138,32 @@ struct GluOp {
     // huge factor
     return !(low < kLow) || abs_max8(t) <= 1e8f;
   }
-  __device__ __forceinline__ double value64(int64_t row, int c, const uint4 *at) const {
-    const uint16_t *g = gate_of(row) + c, *t = g + p.out.n;
-    if (at) {
-      g = reinterpret_cast<const uint16_t *>(at) + c;
-      t = g + 8 * UPT * static_cast<int>(blockDim.x);
-    }
-    return glu64<T, ACT>(g, t, p.smooth ? p.smooth + c : nullptr);
+  __device__ __forceinline__ double value64(int64_t row, int c) const {
+    const uint16_t *g = gate_of(row) + c;
+    return glu64<T, ACT>(g, g + p.out.n, p.smooth ? p.smooth + c : nullptr);
   }
-  // candidates for the maximum: 2^-13 covers the error for every z >= kLow
+  __device__ __forceinline__ void save(double *) const {}
+  __device__ __forceinline__ void restore(int64_t, const double *) const {}
+  // units that may hold the maximum: 2^-13 covers the error for every z >= kLow
   __device__ __forceinline__ float slack(float M) const { return M * 1.220703125e-4f; }
+  static constexpr float kUnit24 = 5.9604644775390625e-8f;  // 2^-24
+  static constexpr float kSlope = ACT == ACT_SILU ? 2.f : 6.f;
+  // the row's maximum is taken to have z >= -2 (coarse() counts on it)
+  __device__ __forceinline__ bool sure(int64_t row, int u, const float2 v[4], float thr, const uint4 *) const {
+    bool ok = true;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (fabsf(elem(v, j)) >= thr) {
+        const float g = Cvt<T>::f1(gate_of(row)[8 * u + j]);
+        ok = ok && arg2(make_float2(g, g)).x >= -2.f;
+      }
+    return ok;
+  }
+  // a value's 9 + slope max(-z, 0), the scale's (the same at z = -2) and 5 for
+  // the scale's and the quotient's roundings
   __device__ __forceinline__ float coarse(const Keep &keep, float) const {
-    return (QT == 1 ? 7.01f : 127.01f) *
-           __fmaf_rn(fminf(-keep.low, -kLow), 4.76837158203125e-7f, 1.1920928955078125e-6f);
+    constexpr float q = (QT == 1 ? 7.01f : 127.01f) * kUnit24;
+    return __fmaf_rn(fminf(-keep.low, -kLow), q * kSlope, q * (24.f + 2.f * kSlope));
   }
 };
 

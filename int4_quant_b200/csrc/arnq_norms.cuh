@@ -104,7 +104,7 @@ struct NormsOp {
   static constexpr int QT = QT_, UPT = UPT_, kInputs = 2;
   static constexpr bool kReadsSlots = false;  // after prepare()
   static constexpr bool FULL = FULL_, VEC = VEC_, STAGED = VEC_ && UPT_ > 0;
-  static constexpr int kMaxThreads = UPT == 4 ? 384 : 1024, kMinCtas = UPT == 4 ? 2 : 1;
+  static constexpr int kMaxThreads = UPT == 4 ? 512 : 1024, kMinCtas = UPT == 4 ? 2 : 1;
   struct Keep {
     float2 f[4];  // the unit's h, then its x'
   };
@@ -129,7 +129,7 @@ struct NormsOp {
       times(v, p.smooth, u);
       b = abs_top8(v, b);
     }
-    bmax = block_max(b, sm.top, nwarps);
+    bmax = block_max(b, sm.top[1], nwarps);
     __syncthreads();  // the slots are used again at once
   }
   __device__ __forceinline__ void times(float2 v[4], const uint16_t *by, int u) const {
@@ -138,6 +138,12 @@ struct NormsOp {
     unpack<T>(load_unit<VEC, false>(by, u, p.out.n), s);
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = __fmul2_rn(v[k], s[k]);
+  }
+  __device__ __forceinline__ void find_gate(int64_t row) {
+    gate_row = p.gate ? p.gate + static_cast<int64_t>(static_cast<uint32_t>(row) /
+                                                      static_cast<uint32_t>(p.rows_per_gate)) *
+                                     p.out.n
+                      : nullptr;
   }
   __device__ __forceinline__ void stage(int64_t row, int u, uint4 *slot, int stride) const {
     const int64_t off = row * p.out.n + 8 * u;
@@ -201,10 +207,7 @@ struct NormsOp {
   __device__ __forceinline__ void prepare(RowSmem &sm, int64_t row, Keep *keep, const uint4 *slot, int nt,
                                           E &&each, int nwarps) {
     const int stride = UPT * nt;
-    gate_row = p.gate ? p.gate + static_cast<int64_t>(static_cast<uint32_t>(row) /
-                                                      static_cast<uint32_t>(p.rows_per_gate)) *
-                                     p.out.n
-                      : nullptr;
+    find_gate(row);
     // ---- Rms of h
     double ss = 0.0;
     each([&](int u, int i) {
@@ -254,7 +257,7 @@ struct NormsOp {
     }
     return !pre.cold;
   }
-  __device__ __forceinline__ double value64(int64_t row, int c, const uint4 *) const {
+  __device__ __forceinline__ double value64(int64_t row, int c) const {
     const int64_t at = row * p.out.n + c;
     const uint16_t x = p.x_out ? p.x_out[at]
                                : x64<T>(p.h[at], p.x[at], p.gamma_post + c, gate_row ? gate_row + c : nullptr,
@@ -265,13 +268,25 @@ struct NormsOp {
     if (p.smooth) y = __dmul_rn(y, static_cast<double>(Cvt<T>::f1(p.smooth[c])));
     return y;
   }
-  // |in - in64| <= |x' inv G| 2^-22 + |in| 2^-24 <= (M + 2 bmax) 2^-21
-  __device__ __forceinline__ float slack(float M) const {
-    return __fmaf_rn(2.f, bmax, M) * 4.76837158203125e-7f;
+  __device__ __forceinline__ void save(double *stat) const {
+    stat[0] = post.inv64;
+    stat[1] = pre.inv64;
   }
-  // (Q + 2 bmax / scale) 2^-20: the same over the scale, and its reciprocal's error
+  __device__ __forceinline__ void restore(int64_t row, const double *stat) {
+    post.inv64 = stat[0];
+    pre.inv64 = stat[1];
+    find_gate(row);
+  }
+  // |in - in64| <= (M + 2 bmax) 4 2^-24: one rounding each of the factor, the
+  // two products and the addition
+  __device__ __forceinline__ float slack(float M) const {
+    return __fmaf_rn(2.f, bmax, M) * 2.384185791015625e-7f;
+  }
+  __device__ __forceinline__ bool sure(int64_t, int, const float2[4], float, const uint4 *) const { return true; }
+  // over the scale: that, the scale's own (4, the same) and 5 for the scale's and
+  // the quotient's roundings; one more for the bound's
   __device__ __forceinline__ float coarse(const Keep &, float inv) const {
-    return __fmaf_rn(2.f * bmax, inv, QT == 1 ? 7.f : 127.f) * 9.5367431640625e-7f;
+    return __fmaf_rn(2.f * bmax, inv, QT == 1 ? 7.f : 127.f) * (14.f * 5.9604644775390625e-8f);
   }
 };
 

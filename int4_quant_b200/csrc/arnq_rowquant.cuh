@@ -13,9 +13,14 @@
 //   - a code is decided in binary32 unless the quotient lies within its error
 //     of a half-way point; the codes of units with such a one are decided by
 //     their fp64 values (code_exact).
-// The fp64 work is done by warps together, eight lanes to a unit, in code kept
-// out of the row's main path, which has to stay in the instruction cache (in
-// line in every unit it cost 217 us instead of 150 on the norms of 8192 x 4096).
+// Neither holds a row up: its codes are written with the binary32 scale, whose
+// distance from the exact one the bound covers, and the units left to decide
+// are listed in a record.  After sixteen rows, or its last, the CTA settles its
+// records, a warp a row and eight lanes a unit: the exact scale, then the codes
+// of the listed units.  (Decided within each row, the maximum's fp64 value and
+// the codes' cost 33 of the 121 us of the gated activation of 4096 x 16384, in
+// latency that every warp of the row waits for; and in line in every unit, out
+// of the instruction cache, the norms of 8192 x 4096 took 217 us instead of 127.)
 // Rows whose maximum is below kTiny, above kHuge or not finite are computed
 // in fp64 throughout.  A row holding a NaN gets scale NaN, one holding an
 // infinity scale infinity (NaN if both), both with codes 0; an all-zero row
@@ -112,12 +117,24 @@ __device__ __forceinline__ double sumsq(const float2 f[4]) {
 
 // ------------------------------------------------------------ block reductions
 
+// What a row leaves to decide in fp64.
+constexpr int kRecords = 16;
+constexpr int kListCap = 48;  // units with codes near a half-way point
+constexpr int kMaxCap = 12;   // units that may hold the maximum
+struct RowRecord {
+  double stat[2];  // what the operator needs for the row's fp64 values
+  int64_t row;
+  int32_t units, tops;        // listed so far (beyond a list's room: the whole row is redone)
+  uint16_t unit[kListCap], top[kMaxCap];
+};
+
 // Slots of one kind of reduction.  Two reductions of the same kind are always
 // separated by a barrier of another kind.
 struct RowSmem {
   double sum[3][32];
-  unsigned top[32];
-  unsigned long long cand[2];  // fp64 maxima of a row, by row parity
+  unsigned top[2][32];       // by row parity
+  unsigned long long cand;   // fp64 maximum of a row that is in fp64 throughout
+  RowRecord rec[kRecords];
 };
 
 // Sum over the CTA (every warp takes part); one barrier, none for one warp.
@@ -212,25 +229,50 @@ __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_grou
 
 // ------------------------------------------------------------ the kernel
 
-// The fp64 values of the units flagged by the lanes of a warp: eight lanes a
-// unit, four units a round.  flags: bit i for the lane's unit first + i*step;
-// use(u, c, in): in = value64(row, c) of column c = 8u + lane % 8 (0 behind the
-// row's end), called by every lane; u < 0 for lanes without a unit.
-template <int NU, class Op, class Use>
-__device__ __forceinline__ void flagged_units(const Op &op, int64_t row, unsigned flags, int first, int step,
-                                              int n, const uint4 *at, Use &&use) {
-  const int lane = threadIdx.x & 31, group = lane >> 3;
+__device__ __forceinline__ float rcp_approx(float y) {
+  float e;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));
+  return e;
+}
+
+// Column c's code into row yr, by the eight lanes of unit u (u < 0: none); all
+// lanes of the warp call it.
+template <int QT>
+__device__ __forceinline__ void put_code(uint8_t *yr, int u, int c, int n, int code) {
+  if (QT == 0) {
+    if (u >= 0 && c < n) yr[c] = static_cast<uint8_t>(code);
+  } else {
+    const int up = __shfl_down_sync(0xFFFFFFFFu, code, 1);
+    if (u >= 0 && c < n && (c & 1) == 0) yr[c >> 1] = static_cast<uint8_t>((code & 0xF) | (up << 4));
+  }
+}
+
+// Settles a row from its record, by one warp.
+template <class Op>
+__device__ __forceinline__ void settle_row(Op &op, const RowRecord &rec, const RowOut &out) {
+  constexpr int Q = Op::QT == 1 ? 7 : 127;
+  const int lane = threadIdx.x & 31, n = out.n;
+  const int64_t row = rec.row;
+  op.restore(row, rec.stat);
+  const bool all_tops = rec.tops > kMaxCap, all_units = rec.units > kListCap;
+  const int tops = all_tops ? out.units : rec.tops, todo = all_units ? out.units : rec.units;
+  double top = 0.0;
 #pragma unroll 1
-  for (int i = 0; i < NU; ++i) {
-    unsigned who = __ballot_sync(0xFFFFFFFFu, (flags >> i) & 1u);
-    while (who) {
-      unsigned mine = who;
-      for (int g = 0; g < group; ++g) mine &= mine - 1u;
-      for (int g = 0; g < 4; ++g) who &= who - 1u;
-      const int u = mine ? first - lane + (__ffs(mine) - 1) + i * step : -1;
-      const int c = 8 * u + (lane & 7);
-      use(u, c, u >= 0 && c < n ? op.value64(row, c, at) : 0.0);
-    }
+  for (int i = lane >> 3; i < tops; i += 4) {
+    const int c = 8 * (all_tops ? i : rec.top[i]) + (lane & 7);
+    if (c < n) top = fmax(top, fabs(op.value64(row, c)));
+  }
+  top = warp_max_d(top);
+  const float sc = __double2float_rn(div_q<Q>(top));
+  if (lane == 0) out.scale[row] = sc;
+  const float inv = rcp_approx(sc);
+  uint8_t *yr = out.y + row * (Op::QT == 1 ? n / 2 : n);
+#pragma unroll 1
+  for (int i0 = 0; i0 < todo; i0 += 4) {
+    const int i = i0 + (lane >> 3);
+    const int u = i < todo ? (all_units ? i : rec.unit[i]) : -1, c = 8 * u + (lane & 7);
+    const double in = u >= 0 && c < n ? op.value64(row, c) : 0.0;
+    put_code<Op::QT>(yr, u, c, n, code_exact(in, sc, __double2float_rn(in) * inv, Q));
   }
 }
 
@@ -244,12 +286,16 @@ __device__ __forceinline__ void flagged_units(const Op &op, int64_t row, unsigne
 //   prepare(...)                    the row's statistics
 //   value(row, u, keep, ..., v)     a unit's binary32 values; returns false
 //                                   where they have no error bound
-//   value64(row, c, at)             one value in fp64, from memory (or the
-//                                   row's slots at `at`, if not null)
+//   value64(row, c)                 one value in fp64, from memory
 //   kReadsSlots                     value() reads the slots too, not prepare()
 //                                   alone: the next row is staged later
 //   slack(M)                        bound on |value - value64| over the row
-//   coarse(keep, inv)               bound on the error of a unit's quotients
+//   sure(row, u, v, thr, slot)      whether the values >= thr of a unit are as
+//                                   near their fp64 values as coarse() takes the
+//                                   row's maximum to be
+//   coarse(keep, inv)               bound on the error of a unit's quotients, that
+//                                   of the binary32 scale included
+//   save(stat), restore(row, stat)  what value64() needs of the row
 template <class Op>
 __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel(const __grid_constant__ typename Op::Params p) {
   constexpr int UPT = Op::UPT, NU = UPT > 0 ? UPT : 1;
@@ -277,26 +323,22 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
       for (int u = tid; u < units; u += nt) f(u, 0);
     }
   };
-  // f(u, i) sets the lane's flag of a unit; then the flagged units in fp64
-  // (`at`: the row's staged inputs where they are still there)
-  auto each_flagged = [&](int64_t row, const uint4 *at, auto &&f, auto &&use) {
-    if (UPT > 0) {
-      unsigned flags = 0u;
-#pragma unroll
-      for (int i = 0; i < NU; ++i) {
-        const int u = tid + i * nt;
-        if ((Op::FULL || u < units) && f(u, i)) flags |= 1u << i;
-      }
-      __syncwarp();
-      if (__any_sync(0xFFFFFFFFu, flags != 0u)) flagged_units<NU>(op, row, flags, tid, nt, n, at, use);
-    } else {
-      for (int u0 = tid & ~31; u0 < units; u0 += nt) {  // whole warps
-        const int u = u0 + (tid & 31);
-        const unsigned flags = u < units && f(u, 0) ? 1u : 0u;
-        __syncwarp();
-        flagged_units<1>(op, row, flags, u, 0, n, at, use);
-      }
+  // use(u, c, value64(row, c)) for every column, by whole warps, eight lanes a unit
+  auto each_unit64 = [&](int64_t r, auto &&use) {
+#pragma unroll 1
+    for (int u0 = (tid >> 5) * 4; u0 < units; u0 += nwarps * 4) {
+      const int u = u0 + ((tid & 31) >> 3) < units ? u0 + ((tid & 31) >> 3) : -1, c = 8 * u + (tid & 7);
+      use(u, c, u >= 0 && c < n ? op.value64(r, c) : 0.0);
     }
+  };
+  auto settle = [&](int count) {
+    __syncthreads();  // the rows' codes, x' and records are written
+    for (int i = tid >> 5; i < count; i += nwarps) {
+      settle_row(op, sm.rec[i], out);
+      __syncwarp();
+      if ((tid & 31) == 0) sm.rec[i].units = sm.rec[i].tops = 0;
+    }
+    __syncthreads();
   };
   int64_t row = blockIdx.x;
   auto stage = [&](int64_t r) {
@@ -308,9 +350,9 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
   };
   stage(row);
   op.setup(sm, tid, nt, nwarps);
-  if (tid < 2) sm.cand[tid] = 0ull;
+  if (tid < kRecords) sm.rec[tid].units = sm.rec[tid].tops = 0;
 
-  int parity = 0;
+  int parity = 0, records = 0;
   for (; row < out.rows; row += gridDim.x, parity ^= 1) {
     typename Op::Keep keep[NU];
     float2 v[NU][4];
@@ -320,19 +362,18 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
 
     if (Op::QT == kQNone) {
       uint16_t *yr = reinterpret_cast<uint16_t *>(out.y) + row * n;
-      each_flagged(
-          row, nullptr,
-          [&](int u, int i) {
-            const bool ok = op.value(row, u, keep[i], slots + i * nt + tid, UPT * nt, v[i]);
-            uint32_t w[4];
+      bool sure = true;
+      each([&](int u, int i) {
+        sure = op.value(row, u, keep[i], slots + i * nt + tid, UPT * nt, v[i]) && sure;
+        uint32_t w[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = Cvt<typename Op::T>::pack(v[i][k].x, v[i][k].y);
-            store_unit<VEC>(yr, u, n, make_uint4(w[0], w[1], w[2], w[3]));
-            return !ok;
-          },
-          [&](int u, int c, double in) {
-            if (u >= 0 && c < n) yr[c] = round16<typename Op::T>(in);
-          });
+        for (int k = 0; k < 4; ++k) w[k] = Cvt<typename Op::T>::pack(v[i][k].x, v[i][k].y);
+        store_unit<VEC>(yr, u, n, make_uint4(w[0], w[1], w[2], w[3]));
+      });
+      if (__syncthreads_or(!sure))  // (a property of the row)
+        each_unit64(row, [&](int u, int c, double in) {
+          if (u >= 0 && c < n) yr[c] = round16<typename Op::T>(in);
+        });
       continue;
     }
 
@@ -342,91 +383,99 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
       if (!op.value(row, u, keep[i], slots + i * nt + tid, UPT * nt, v[i])) top32 = __int_as_float(0x7F800000);
       top32 = abs_top8(v[i], top32);
     });
-    const float M = block_max(top32, sm.top, nwarps);
-    const bool wide = !(M >= kTiny && M <= kHuge);  // the whole row in fp64
-    if (tid == 0) sm.cand[parity ^ 1] = 0ull;       // the next row's
-
-    // ---- fp64 maximum over the units that may hold it
-    const float thr = M - 2.f * op.slack(M);
-    if (__any_sync(0xFFFFFFFFu, wide || top32 >= thr)) {
-      unsigned long long best = 0ull;
-      each_flagged(
-          row, Op::STAGED && Op::kReadsSlots ? slots : nullptr,
-          [&](int u, int i) {
-            if (UPT == 0) op.value(row, u, keep[i], slots, 0, v[i]);
-            return wide || abs_max8(v[i]) >= thr;
-          },
-          [&](int, int, double in) {
-            best = max(best, static_cast<unsigned long long>(__double_as_longlong(fabs(in))));
-          });
-      if (best) atomicMax(&sm.cand[parity], best);
-    }
-    __syncthreads();
-    if (Op::kReadsSlots) stage(row + gridDim.x);
-    const double top = __longlong_as_double(static_cast<long long>(sm.cand[parity]));
-    const float sc = __double2float_rn(wide ? div_ieee(top, static_cast<double>(Q)) : div_q<Q>(top));
-    if (tid == 0) out.scale[row] = sc;
-    const bool finite = sc > 0.f && sc <= 3.402823466e38f;  // else every code is 0
-    const float inv = __fdividef(1.f, sc);
-
-    // ---- codes
+    const float M = block_max(top32, sm.top[parity], nwarps);
+    RowRecord &rec = sm.rec[records];
     const int64_t code_bytes = Op::QT == 1 ? n / 2 : n;
     uint8_t *yr = out.y + row * code_bytes;
-    each_flagged(
-        row, nullptr,
-        [&](int u, int i) {
-          if (UPT == 0) op.value(row, u, keep[i], slots, 0, v[i]);
-          // t = value/scale; adding kMagic rounds it to a whole number whose
-          // low bits are the code; what was rounded off tells how near a
-          // half-way point it was
-          uint32_t q[8];
-          float off = 0.f;
-          const float2 inv2 = make_float2(inv, inv), mag = make_float2(kMagic, kMagic),
-                       neg = make_float2(-kMagic, -kMagic), minus = make_float2(-1.f, -1.f);
+    const bool wide = !(M >= kTiny && M <= kHuge);
+    if (wide) {
+      // ---- the whole row in fp64
+      if (Op::kReadsSlots) stage(row + gridDim.x);
+      if (tid == 0) sm.cand = 0ull;
+      __syncthreads();
+      unsigned long long best = 0ull;
+      each_unit64(row, [&](int, int, double in) {
+        best = max(best, static_cast<unsigned long long>(__double_as_longlong(fabs(in))));
+      });
+      if (best) atomicMax(&sm.cand, best);
+      __syncthreads();
+      const float sc = __double2float_rn(
+          div_ieee(__longlong_as_double(static_cast<long long>(sm.cand)), static_cast<double>(Q)));
+      const bool finite = sc > 0.f && sc <= 3.402823466e38f;  // else every code is 0
+      if (tid == 0) out.scale[row] = sc;
+      each_unit64(row, [&](int u, int c, double in) {
+        put_code<Op::QT>(yr, u, c, n,
+                         finite && in == in ? code_of_t(div_ieee(in, static_cast<double>(sc)), Q) : 0);
+      });
+      continue;
+    }
+
+    // ---- units that may hold the maximum, listed
+    if (top32 >= M - 2.f * op.slack(M)) {
+      each([&](int u, int i) {
+        if (UPT == 0) op.value(row, u, keep[i], slots, 0, v[i]);
+        if (abs_max8(v[i]) < M - 2.f * op.slack(M)) return;
+        const int at = atomicAdd(&rec.tops, op.sure(row, u, v[i], M - 2.f * op.slack(M), slots + i * nt + tid) ? 1 : kMaxCap + 1);
+        if (at < kMaxCap) rec.top[at] = static_cast<uint16_t>(u);
+      });
+    }
+    if (Op::kReadsSlots) stage(row + gridDim.x);  // this row's slots have been read, behind a barrier
+    if (tid == 0) {
+      op.save(rec.stat);
+      rec.row = row;
+    }
+
+    // ---- codes, with the binary32 scale
+    const float inv = rcp_approx(M * (1.f / Q));
+    each([&](int u, int i) {
+      if (UPT == 0) op.value(row, u, keep[i], slots, 0, v[i]);
+      // t = value/scale; adding kMagic rounds it to a whole number whose
+      // low bits are the code; what was rounded off tells how near a
+      // half-way point it was
+      uint32_t q[8];
+      float off = 0.f;
+      const float2 inv2 = make_float2(inv, inv), mag = make_float2(kMagic, kMagic),
+                   neg = make_float2(-kMagic, -kMagic), minus = make_float2(-1.f, -1.f);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 t = __fmul2_rn(v[i][k], inv2);
-            const float2 r = __fadd2_rn(t, mag);
-            const float2 d = __ffma2_rn(__fadd2_rn(r, neg), minus, t);
-            off = abs_max3(d.x, d.y, off);
-            q[2 * k] = __float_as_uint(r.x);
-            q[2 * k + 1] = __float_as_uint(r.y);
-          }
-          uint32_t lo, hi;  // eight codes, column 0 lowest
-          if (Op::QT == 0) {
-            lo = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
-            hi = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
-          } else {
-            const uint32_t even = __byte_perm(__byte_perm(q[0], q[2], 0x0040), __byte_perm(q[4], q[6], 0x0040), 0x5410);
-            const uint32_t odd = __byte_perm(__byte_perm(q[1], q[3], 0x0040), __byte_perm(q[5], q[7], 0x0040), 0x5410);
-            lo = (even & 0x0F0F0F0Fu) | ((odd << 4) & 0xF0F0F0F0u);
-            hi = 0u;
-          }
-          if (VEC) {
-            if (Op::QT == 0) reinterpret_cast<uint2 *>(yr)[u] = make_uint2(lo, hi);
-            else reinterpret_cast<uint32_t *>(yr)[u] = lo;
-          } else {
-            const int cnt = min(8, n - 8 * u), bytes = Op::QT == 0 ? cnt : cnt / 2;
-            uint8_t *to = yr + static_cast<int64_t>(u) * (Op::QT == 0 ? 8 : 4);
+      for (int k = 0; k < 4; ++k) {
+        const float2 t = __fmul2_rn(v[i][k], inv2);
+        const float2 r = __fadd2_rn(t, mag);
+        const float2 d = __ffma2_rn(__fadd2_rn(r, neg), minus, t);
+        off = abs_max3(d.x, d.y, off);
+        q[2 * k] = __float_as_uint(r.x);
+        q[2 * k + 1] = __float_as_uint(r.y);
+      }
+      uint32_t lo, hi;  // eight codes, column 0 lowest
+      if (Op::QT == 0) {
+        lo = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+        hi = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
+      } else {
+        const uint32_t even = __byte_perm(__byte_perm(q[0], q[2], 0x0040), __byte_perm(q[4], q[6], 0x0040), 0x5410);
+        const uint32_t odd = __byte_perm(__byte_perm(q[1], q[3], 0x0040), __byte_perm(q[5], q[7], 0x0040), 0x5410);
+        lo = (even & 0x0F0F0F0Fu) | ((odd << 4) & 0xF0F0F0F0u);
+        hi = 0u;
+      }
+      if (VEC) {
+        if (Op::QT == 0) reinterpret_cast<uint2 *>(yr)[u] = make_uint2(lo, hi);
+        else reinterpret_cast<uint32_t *>(yr)[u] = lo;
+      } else {
+        const int cnt = min(8, n - 8 * u), bytes = Op::QT == 0 ? cnt : cnt / 2;
+        uint8_t *to = yr + static_cast<int64_t>(u) * (Op::QT == 0 ? 8 : 4);
 #pragma unroll
-            for (int j = 0; j < (Op::QT == 0 ? 8 : 4); ++j)
-              if (j < bytes) to[j] = static_cast<uint8_t>((j < 4 ? lo : hi) >> (8 * (j & 3)));
-          }
-          return wide || off >= 0.5f - op.coarse(keep[i], inv);
-        },
-        [&](int u, int c, double in) {
-          int code = 0;
-          if (finite && in == in)
-            code = wide ? code_of_t(div_ieee(in, static_cast<double>(sc)), Q)
-                        : code_exact(in, sc, __double2float_rn(in) * inv, Q);
-          if (Op::QT == 0) {
-            if (u >= 0 && c < n) yr[c] = static_cast<uint8_t>(code);
-          } else {
-            const int up = __shfl_down_sync(0xFFFFFFFFu, code, 1);
-            if (u >= 0 && c < n && (c & 1) == 0) yr[c >> 1] = static_cast<uint8_t>((code & 0xF) | (up << 4));
-          }
-        });
+        for (int j = 0; j < (Op::QT == 0 ? 8 : 4); ++j)
+          if (j < bytes) to[j] = static_cast<uint8_t>((j < 4 ? lo : hi) >> (8 * (j & 3)));
+      }
+      if (off >= 0.5f - op.coarse(keep[i], inv)) {
+        const int at = atomicAdd(&rec.units, 1);
+        if (at < kListCap) rec.unit[at] = static_cast<uint16_t>(u);
+      }
+    });
+    if (++records == kRecords) {
+      settle(records);
+      records = 0;
+    }
   }
+  if (Op::QT != kQNone) settle(records);
   // the next kernel on the stream may start its set-up (it waits for this
   // grid's completion before touching memory)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
