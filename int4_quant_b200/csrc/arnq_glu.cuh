@@ -113,12 +113,13 @@ struct GluOp {
       unpack<T>(slot[0], g);
       unpack<T>(slot[stride], t);
     } else {
-      unpack<T>(load_unit<VEC, false>(gate_of(row), u, p.out.n), g);
-      unpack<T>(load_unit<VEC, false>(gate_of(row) + p.out.n, u, p.out.n), t);
+      const int64_t n = p.out.n, all = p.out.rows * (2 * n);
+      unpack<T>(load_unit<VEC>(p.x, row * (2 * n), u, p.out.n, all), g);
+      unpack<T>(load_unit<VEC>(p.x, row * (2 * n) + n, u, p.out.n, all), t);
     }
     if (p.smooth) {
       float2 s[4];
-      unpack<T>(load_unit<VEC, false>(p.smooth, u, p.out.n), s);
+      unpack<T>(load_unit<VEC>(p.smooth, 0, u, p.out.n, p.out.n), s);
 #pragma unroll
       for (int k = 0; k < 4; ++k) t[k] = __fmul2_rn(t[k], s[k]);  // exact
     }

@@ -79,7 +79,7 @@ extern "C" arnq_status arnq_post_norm_add_rms_norm_dynamic_quant(
   int dev = 0, sms = 0, upt = 0, threads = 0;
   st = current_device(&dev, &sms);
   if (st != ARNQ_OK) return st;
-  row_threads(p.out.units, rows > sms, 512, &upt, &threads);
+  row_threads(p.out.units, rows > sms, qt == kQNone ? 288 : 384, &upt, &threads);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return dt == ARNQ_BF16 ? by_codes<Bf16>(p, qt, vec, upt, threads, s)
                          : by_codes<Fp16>(p, qt, vec, upt, threads, s);

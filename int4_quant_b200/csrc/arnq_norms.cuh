@@ -104,7 +104,8 @@ struct NormsOp {
   static constexpr int QT = QT_, UPT = UPT_, kInputs = 2;
   static constexpr bool kReadsSlots = false;  // after prepare()
   static constexpr bool FULL = FULL_, VEC = VEC_, STAGED = VEC_ && UPT_ > 0;
-  static constexpr int kMaxThreads = UPT == 4 ? 512 : 1024, kMinCtas = UPT == 4 ? 2 : 1;
+  static constexpr int kMaxThreads = UPT == 4 ? (QT == kQNone ? 288 : 384) : 1024,
+                       kMinCtas = UPT == 4 ? (QT == kQNone ? 3 : 2) : 1;
   struct Keep {
     float2 f[4];  // the unit's h, then its x'
   };
@@ -125,7 +126,7 @@ struct NormsOp {
     float b = 0.f;
     for (int u = tid; u < p.out.units; u += nt) {
       float2 v[4];
-      unpack<T>(load_unit<VEC, false>(p.beta, u, p.out.n), v);
+      unpack<T>(load_unit<VEC>(p.beta, 0, u, p.out.n, p.out.n), v);
       times(v, p.smooth, u);
       b = abs_top8(v, b);
     }
@@ -135,7 +136,7 @@ struct NormsOp {
   __device__ __forceinline__ void times(float2 v[4], const uint16_t *by, int u) const {
     if (!by) return;
     float2 s[4];
-    unpack<T>(load_unit<VEC, false>(by, u, p.out.n), s);
+    unpack<T>(load_unit<VEC>(by, 0, u, p.out.n, p.out.n), s);
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = __fmul2_rn(v[k], s[k]);
   }
@@ -151,15 +152,15 @@ struct NormsOp {
     copy16_async(slot + stride, p.x + off);
   }
   __device__ __forceinline__ uint4 get_h(int64_t row, int u, const uint4 *slot) const {
-    return STAGED ? slot[0] : load_unit<VEC, false>(p.h + row * p.out.n, u, p.out.n);
+    return STAGED ? slot[0] : load_unit<VEC>(p.h, row * p.out.n, u, p.out.n, p.out.rows * p.out.n);
   }
   __device__ __forceinline__ uint4 get_x(int64_t row, int u, const uint4 *slot, int stride) const {
-    return STAGED ? slot[stride] : load_unit<VEC, false>(p.x + row * p.out.n, u, p.out.n);
+    return STAGED ? slot[stride] : load_unit<VEC>(p.x, row * p.out.n, u, p.out.n, p.out.rows * p.out.n);
   }
   // long rows: x' of a unit after the row's first phases, read back or made again
   __device__ __forceinline__ void x_again(int64_t row, int u, Keep &keep) const {
     if (p.x_out) {
-      unpack<T>(load_unit<VEC, false>(p.x_out + row * p.out.n, u, p.out.n), keep.f);
+      unpack<T>(load_unit<VEC>(p.x_out, row * p.out.n, u, p.out.n, p.out.rows * p.out.n), keep.f);
     } else {
       unpack<T>(get_h(row, u, nullptr), keep.f);
       make_x(row, u, keep, nullptr, 0);
@@ -171,7 +172,7 @@ struct NormsOp {
     float2 x[4], G[4];
     const uint4 xw = get_x(row, u, slot, stride);
     unpack<T>(xw, x);
-    unpack<T>(load_unit<VEC, false>(p.gamma_post, u, p.out.n), G);
+    unpack<T>(load_unit<VEC>(p.gamma_post, 0, u, p.out.n, p.out.n), G);
     times(G, gate_row, u);
     const float2 f = make_float2(post.inv, post.inv);
     float2 v[4];
@@ -243,11 +244,11 @@ struct NormsOp {
   __device__ __forceinline__ bool value(int64_t row, int u, Keep &keep, const uint4 *, int, float2 v[4]) const {
     if (UPT == 0) x_again(row, u, keep);
     float2 G[4], B[4];
-    unpack<T>(load_unit<VEC, false>(p.gamma, u, p.out.n), G);
+    unpack<T>(load_unit<VEC>(p.gamma, 0, u, p.out.n, p.out.n), G);
     times(G, p.smooth, u);
     const float2 r = make_float2(pre.inv, pre.inv);
     if (p.beta) {
-      unpack<T>(load_unit<VEC, false>(p.beta, u, p.out.n), B);
+      unpack<T>(load_unit<VEC>(p.beta, 0, u, p.out.n, p.out.n), B);
       times(B, p.smooth, u);
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = __ffma2_rn(__fmul2_rn(keep.f[k], r), G[k], B[k]);

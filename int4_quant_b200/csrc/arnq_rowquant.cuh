@@ -16,8 +16,8 @@
 // Neither holds a row up: its codes are written with the binary32 scale, whose
 // distance from the exact one the bound covers, and the units left to decide
 // are listed in a record.  After sixteen rows, or its last, the CTA settles its
-// records, a warp a row and eight lanes a unit: the exact scale, then the codes
-// of the listed units.  (Decided within each row, the maximum's fp64 value and
+// records, eight lanes a row for the exact scales, then eight lanes a listed
+// unit for its codes.  (Decided within each row, the maximum's fp64 value and
 // the codes' cost 33 of the 121 us of the gated activation of 4096 x 16384, in
 // latency that every warp of the row waits for; and in line in every unit, out
 // of the instruction cache, the norms of 8192 x 4096 took 217 us instead of 127.)
@@ -54,21 +54,46 @@ __device__ __forceinline__ void set16(uint4 &w, int j, uint16_t v) {
   if ((j >> 1) == 3) w.w = (w.w & keep) | put;
 }
 
-// Elements 8u .. 8u+7 of a row of n starting at `row`; zeros past its end.
-// VEC: the row is 16-byte aligned and n a multiple of 8.
-template <bool VEC, bool STREAM>
-__device__ __forceinline__ uint4 load_unit(const uint16_t *row, int u, int n) {
-  if (VEC) return STREAM ? ld_stream16(row + 8 * static_cast<int64_t>(u))
-                         : *reinterpret_cast<const uint4 *>(row + 8 * static_cast<int64_t>(u));
-  uint32_t w[4];
-  const int c = 8 * u;
+// Elements 8u .. 8u+7 of a row of n that starts `at` elements into an array of
+// `count`; zeros past the row's end.  VEC: 16-byte aligned, n a multiple of 8.
+// Otherwise two aligned 16-byte loads around the unit, shifted into place, or,
+// where they would leave the array, one element at a time.
+template <bool VEC>
+__device__ __forceinline__ uint4 load_unit(const uint16_t *array, int64_t at, int u, int n, int64_t count) {
+  const uint16_t *p = array + at + 8 * static_cast<int64_t>(u);
+  if (VEC) return *reinterpret_cast<const uint4 *>(p);
+  const int left = n - 8 * u;  // elements of the unit that exist
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), q = a & ~static_cast<uintptr_t>(15);
+  const uint32_t off = static_cast<uint32_t>(a & 15);
+  uint32_t r[4];
+  if (q >= reinterpret_cast<uintptr_t>(array) &&
+      q + (off ? 32 : 16) <= reinterpret_cast<uintptr_t>(array + count)) {
+    const uint4 lo = *reinterpret_cast<const uint4 *>(q);
+    const uint4 hi = off ? *reinterpret_cast<const uint4 *>(q + 16) : lo;
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    if (off & 8) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = c + 2 * i < n ? row[c + 2 * i] : 0u;
-    const uint32_t hi = c + 2 * i + 1 < n ? row[c + 2 * i + 1] : 0u;
-    w[i] = lo | hi << 16;
+      for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (off & 4) {
+#pragma unroll
+      for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __funnelshift_r(w[i], w[i + 1], (off & 2) * 8);
+    if (left < 8) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        r[i] &= (left > 2 * i ? 0xFFFFu : 0u) | (left > 2 * i + 1 ? 0xFFFF0000u : 0u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = left > 2 * i ? p[2 * i] : 0u, y = left > 2 * i + 1 ? p[2 * i + 1] : 0u;
+      r[i] = x | y << 16;
+    }
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 template <bool VEC>
@@ -124,6 +149,7 @@ constexpr int kMaxCap = 12;   // units that may hold the maximum
 struct RowRecord {
   double stat[2];  // what the operator needs for the row's fp64 values
   int64_t row;
+  float scale;
   int32_t units, tops;        // listed so far (beyond a list's room: the whole row is redone)
   uint16_t unit[kListCap], top[kMaxCap];
 };
@@ -235,45 +261,66 @@ __device__ __forceinline__ float rcp_approx(float y) {
   return e;
 }
 
-// Column c's code into row yr, by the eight lanes of unit u (u < 0: none); all
-// lanes of the warp call it.
+// Column c's code into row yr, by the eight lanes of unit u (u < 0: none), all
+// of which call it.
 template <int QT>
 __device__ __forceinline__ void put_code(uint8_t *yr, int u, int c, int n, int code) {
   if (QT == 0) {
     if (u >= 0 && c < n) yr[c] = static_cast<uint8_t>(code);
   } else {
-    const int up = __shfl_down_sync(0xFFFFFFFFu, code, 1);
+    const int up = __shfl_down_sync(0xFFu << (threadIdx.x & 24), code, 1, 8);
     if (u >= 0 && c < n && (c & 1) == 0) yr[c >> 1] = static_cast<uint8_t>((code & 0xF) | (up << 4));
   }
 }
 
-// Settles a row from its record, by one warp.
+// Settles `count` records: eight lanes a row find its scale, then the units
+// listed in all of them are decided, eight lanes a unit.
 template <class Op>
-__device__ __forceinline__ void settle_row(Op &op, const RowRecord &rec, const RowOut &out) {
+__device__ __forceinline__ void settle_rows(Op &op, RowRecord *recs, int count, const RowOut &out) {
   constexpr int Q = Op::QT == 1 ? 7 : 127;
-  const int lane = threadIdx.x & 31, n = out.n;
-  const int64_t row = rec.row;
-  op.restore(row, rec.stat);
-  const bool all_tops = rec.tops > kMaxCap, all_units = rec.units > kListCap;
-  const int tops = all_tops ? out.units : rec.tops, todo = all_units ? out.units : rec.units;
-  double top = 0.0;
+  const int lane = threadIdx.x & 7, group = threadIdx.x >> 3, groups = blockDim.x >> 3, n = out.n;
+  const unsigned mask = 0xFFu << (threadIdx.x & 24);
+  __syncthreads();  // the rows' codes, x' and records are written
 #pragma unroll 1
-  for (int i = lane >> 3; i < tops; i += 4) {
-    const int c = 8 * (all_tops ? i : rec.top[i]) + (lane & 7);
-    if (c < n) top = fmax(top, fabs(op.value64(row, c)));
-  }
-  top = warp_max_d(top);
-  const float sc = __double2float_rn(div_q<Q>(top));
-  if (lane == 0) out.scale[row] = sc;
-  const float inv = rcp_approx(sc);
-  uint8_t *yr = out.y + row * (Op::QT == 1 ? n / 2 : n);
+  for (int r = group; r < count; r += groups) {
+    RowRecord &rec = recs[r];
+    op.restore(rec.row, rec.stat);
+    const bool all = rec.tops > kMaxCap;
+    const int tops = all ? out.units : rec.tops;
+    double top = 0.0;
 #pragma unroll 1
-  for (int i0 = 0; i0 < todo; i0 += 4) {
-    const int i = i0 + (lane >> 3);
-    const int u = i < todo ? (all_units ? i : rec.unit[i]) : -1, c = 8 * u + (lane & 7);
-    const double in = u >= 0 && c < n ? op.value64(row, c) : 0.0;
-    put_code<Op::QT>(yr, u, c, n, code_exact(in, sc, __double2float_rn(in) * inv, Q));
+    for (int i = 0; i < tops; ++i) {
+      const int c = 8 * (all ? i : rec.top[i]) + lane;
+      if (c < n) top = fmax(top, fabs(op.value64(rec.row, c)));
+    }
+    top = group_max_d(top, mask, 8);
+    if (lane == 0) {
+      rec.scale = __double2float_rn(div_q<Q>(top));
+      out.scale[rec.row] = rec.scale;
+    }
   }
+  __syncthreads();
+  int r = 0, before = 0;  // the record that holds item i, and the items of those before it
+#pragma unroll 1
+  for (int i = group;; i += groups) {
+    int here = 0;
+    for (; r < count; ++r) {
+      here = recs[r].units > kListCap ? out.units : recs[r].units;
+      if (i < before + here) break;
+      before += here;
+    }
+    if (r >= count) break;
+    const RowRecord &rec = recs[r];
+    op.restore(rec.row, rec.stat);
+    const int u = rec.units > kListCap ? i - before : rec.unit[i - before], c = 8 * u + lane;
+    const float sc = rec.scale;
+    const double in = c < n ? op.value64(rec.row, c) : 0.0;
+    __syncwarp(mask);
+    put_code<Op::QT>(out.y + rec.row * (Op::QT == 1 ? n / 2 : n), u, c, n,
+                     code_exact(in, sc, __double2float_rn(in) * rcp_approx(sc), Q));
+  }
+  __syncthreads();
+  if (threadIdx.x < count) recs[threadIdx.x].units = recs[threadIdx.x].tops = 0;
 }
 
 // Op: struct with
@@ -330,15 +377,6 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
       const int u = u0 + ((tid & 31) >> 3) < units ? u0 + ((tid & 31) >> 3) : -1, c = 8 * u + (tid & 7);
       use(u, c, u >= 0 && c < n ? op.value64(r, c) : 0.0);
     }
-  };
-  auto settle = [&](int count) {
-    __syncthreads();  // the rows' codes, x' and records are written
-    for (int i = tid >> 5; i < count; i += nwarps) {
-      settle_row(op, sm.rec[i], out);
-      __syncwarp();
-      if ((tid & 31) == 0) sm.rec[i].units = sm.rec[i].tops = 0;
-    }
-    __syncthreads();
   };
   int64_t row = blockIdx.x;
   auto stage = [&](int64_t r) {
@@ -471,11 +509,11 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
       }
     });
     if (++records == kRecords) {
-      settle(records);
+      settle_rows(op, sm.rec, records, out);
       records = 0;
     }
   }
-  if (Op::QT != kQNone) settle(records);
+  if (Op::QT != kQNone) settle_rows(op, sm.rec, records, out);
   // the next kernel on the stream may start its set-up (it waits for this
   // grid's completion before touching memory)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
