@@ -5,35 +5,37 @@
 namespace {
 using namespace arnq;
 
-template <class T, int ACT, int QT, bool VEC>
+template <class T, int ACT, int QT, int MODE>
 arnq_status by_upt(const GluParams &p, int upt, int threads, cudaStream_t s) {
-  if constexpr (VEC) {
+  if constexpr (MODE == WIDE) {
     if (p.out.units == upt * threads) {
-      if (upt == 1) return launch_rows<GluOp<T, ACT, QT, VEC, 1, true>>(p, threads, s);
-      if (upt == 2) return launch_rows<GluOp<T, ACT, QT, VEC, 2, true>>(p, threads, s);
-      if (upt == 4) return launch_rows<GluOp<T, ACT, QT, VEC, 4, true>>(p, threads, s);
+      if (upt == 1) return launch_rows<GluOp<T, ACT, QT, MODE, 1, true>>(p, threads, s);
+      if (upt == 2) return launch_rows<GluOp<T, ACT, QT, MODE, 2, true>>(p, threads, s);
+      if (upt == 4) return launch_rows<GluOp<T, ACT, QT, MODE, 4, true>>(p, threads, s);
     }
+    if (upt == 2) return launch_rows<GluOp<T, ACT, QT, MODE, 2>>(p, threads, s);
   }
-  if (upt == 1) return launch_rows<GluOp<T, ACT, QT, VEC, 1>>(p, threads, s);
-  if (upt == 2) return launch_rows<GluOp<T, ACT, QT, VEC, 2>>(p, threads, s);
-  if (upt == 4) return launch_rows<GluOp<T, ACT, QT, VEC, 4>>(p, threads, s);
-  return launch_rows<GluOp<T, ACT, QT, VEC, 0>>(p, threads, s);
+  if (upt == 1) return launch_rows<GluOp<T, ACT, QT, MODE, 1>>(p, threads, s);
+  if (upt == 4) return launch_rows<GluOp<T, ACT, QT, MODE, 4>>(p, threads, s);
+  return launch_rows<GluOp<T, ACT, QT, MODE, 0>>(p, threads, s);
 }
 template <class T, int ACT, int QT>
-arnq_status by_vec(const GluParams &p, bool vec, int upt, int threads, cudaStream_t s) {
-  return vec ? by_upt<T, ACT, QT, true>(p, upt, threads, s)
-             : by_upt<T, ACT, QT, false>(p, upt, threads, s);
+arnq_status by_mode(const GluParams &p, int mode, int upt, int threads, cudaStream_t s) {
+  if (mode == WIDE) return by_upt<T, ACT, QT, WIDE>(p, upt, threads, s);
+  if constexpr (QT != 1)
+    if (mode == ONES) return by_upt<T, ACT, QT, ONES>(p, upt, threads, s);
+  return by_upt<T, ACT, QT, PAIRS>(p, upt, threads, s);
 }
 template <class T, int ACT>
-arnq_status by_codes(const GluParams &p, int qt, bool vec, int upt, int threads, cudaStream_t s) {
-  return qt == 0 ? by_vec<T, ACT, 0>(p, vec, upt, threads, s)
-                 : by_vec<T, ACT, 1>(p, vec, upt, threads, s);
+arnq_status by_codes(const GluParams &p, int qt, int mode, int upt, int threads, cudaStream_t s) {
+  return qt == 0 ? by_mode<T, ACT, 0>(p, mode, upt, threads, s)
+                 : by_mode<T, ACT, 1>(p, mode, upt, threads, s);
 }
 template <class T>
-arnq_status by_act(const GluParams &p, int act, int qt, bool vec, int upt, int threads,
+arnq_status by_act(const GluParams &p, int act, int qt, int mode, int upt, int threads,
                    cudaStream_t s) {
-  return act == ARNQ_SILU ? by_codes<T, ACT_SILU>(p, qt, vec, upt, threads, s)
-                          : by_codes<T, ACT_GELU_TANH>(p, qt, vec, upt, threads, s);
+  return act == ARNQ_SILU ? by_codes<T, ACT_SILU>(p, qt, mode, upt, threads, s)
+                          : by_codes<T, ACT_GELU_TANH>(p, qt, mode, upt, threads, s);
 }
 }  // namespace
 
@@ -52,7 +54,6 @@ extern "C" arnq_status arnq_glu_dynamic_quant(const void *x, const void *smooth,
   p.out.scale = scale;
   p.out.rows = rows;
   p.out.n = static_cast<int32_t>(n);
-  p.out.units = static_cast<int32_t>(div_up(n, 8));
   p.x = static_cast<const uint16_t *>(x);
   p.smooth = static_cast<const uint16_t *>(smooth);
   const int qt = kernel_qt(qdt);
@@ -61,8 +62,10 @@ extern "C" arnq_status arnq_glu_dynamic_quant(const void *x, const void *smooth,
   int dev = 0, sms = 0, upt = 0, threads = 0;
   st = current_device(&dev, &sms);
   if (st != ARNQ_OK) return st;
-  row_threads(p.out.units, rows > sms, 512, &upt, &threads);
+  const int mode = vec ? WIDE : n % 2 == 0 ? PAIRS : ONES;
+  p.out.units = units_of(mode, p.out.n);
+  row_threads(p.out.units, mode == WIDE, rows > sms, 512, &upt, &threads);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return dt == ARNQ_BF16 ? by_act<Bf16>(p, act, qt, vec, upt, threads, s)
-                         : by_act<Fp16>(p, act, qt, vec, upt, threads, s);
+  return dt == ARNQ_BF16 ? by_act<Bf16>(p, act, qt, mode, upt, threads, s)
+                         : by_act<Fp16>(p, act, qt, mode, upt, threads, s);
 }

@@ -69,13 +69,14 @@ __device__ __noinline__ double glu64(const uint16_t *gate, const uint16_t *up, c
   return smooth ? in * static_cast<double>(Cvt<T>::f1(*smooth)) : in;
 }
 
-template <class T_, int ACT, int QT_, bool VEC_, int UPT_, bool FULL_ = false>
+template <class T_, int ACT, int QT_, int MODE_, int UPT_, bool FULL_ = false>
 struct GluOp {
   typedef T_ T;
   typedef GluParams Params;
   static constexpr int QT = QT_, UPT = UPT_, kInputs = 2;
   static constexpr bool kReadsSlots = true;
-  static constexpr bool FULL = FULL_, VEC = VEC_, STAGED = VEC_ && UPT_ > 0;
+  static constexpr int MODE = MODE_;
+  static constexpr bool FULL = FULL_, STAGED = MODE_ == WIDE && UPT_ > 0;
   static constexpr int kMaxThreads = UPT == 4 ? 512 : 1024, kMinCtas = UPT == 4 ? 2 : 1;
   struct Keep {
     float low;  // the unit's smallest z, at most 0
@@ -113,13 +114,12 @@ struct GluOp {
       unpack<T>(slot[0], g);
       unpack<T>(slot[stride], t);
     } else {
-      const int64_t n = p.out.n, all = p.out.rows * (2 * n);
-      unpack<T>(load_unit<VEC>(p.x, row * (2 * n), u, p.out.n, all), g);
-      unpack<T>(load_unit<VEC>(p.x, row * (2 * n) + n, u, p.out.n, all), t);
+      unpack<T>(load_unit<MODE>(gate_of(row), u, p.out.n), g);
+      unpack<T>(load_unit<MODE>(gate_of(row) + p.out.n, u, p.out.n), t);
     }
     if (p.smooth) {
       float2 s[4];
-      unpack<T>(load_unit<VEC>(p.smooth, 0, u, p.out.n, p.out.n), s);
+      unpack<T>(load_unit<MODE>(p.smooth, u, p.out.n), s);
 #pragma unroll
       for (int k = 0; k < 4; ++k) t[k] = __fmul2_rn(t[k], s[k]);  // exact
     }
@@ -155,7 +155,7 @@ struct GluOp {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (fabsf(elem(v, j)) >= thr) {
-        const float g = Cvt<T>::f1(gate_of(row)[8 * u + j]);
+        const float g = Cvt<T>::f1(gate_of(row)[column<MODE>(u, j)]);
         ok = ok && arg2(make_float2(g, g)).x >= -2.f;
       }
     return ok;

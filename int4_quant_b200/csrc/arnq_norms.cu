@@ -6,29 +6,32 @@
 namespace {
 using namespace arnq;
 
-template <class T, int QT, bool VEC>
+template <class T, int QT, int MODE>
 arnq_status by_upt(const NormsParams &p, int upt, int threads, cudaStream_t s) {
-  if constexpr (VEC) {
+  if constexpr (MODE == WIDE) {
     if (p.out.units == upt * threads) {
-      if (upt == 1) return launch_rows<NormsOp<T, QT, VEC, 1, true>>(p, threads, s);
-      if (upt == 2) return launch_rows<NormsOp<T, QT, VEC, 2, true>>(p, threads, s);
-      if (upt == 4) return launch_rows<NormsOp<T, QT, VEC, 4, true>>(p, threads, s);
+      if (upt == 1) return launch_rows<NormsOp<T, QT, MODE, 1, true>>(p, threads, s);
+      if (upt == 2) return launch_rows<NormsOp<T, QT, MODE, 2, true>>(p, threads, s);
+      if (upt == 4) return launch_rows<NormsOp<T, QT, MODE, 4, true>>(p, threads, s);
     }
+    if (upt == 2) return launch_rows<NormsOp<T, QT, MODE, 2>>(p, threads, s);
   }
-  if (upt == 1) return launch_rows<NormsOp<T, QT, VEC, 1>>(p, threads, s);
-  if (upt == 2) return launch_rows<NormsOp<T, QT, VEC, 2>>(p, threads, s);
-  if (upt == 4) return launch_rows<NormsOp<T, QT, VEC, 4>>(p, threads, s);
-  return launch_rows<NormsOp<T, QT, VEC, 0>>(p, threads, s);
+  if (upt == 1) return launch_rows<NormsOp<T, QT, MODE, 1>>(p, threads, s);
+  if (upt == 4) return launch_rows<NormsOp<T, QT, MODE, 4>>(p, threads, s);
+  return launch_rows<NormsOp<T, QT, MODE, 0>>(p, threads, s);
 }
 template <class T, int QT>
-arnq_status by_vec(const NormsParams &p, bool vec, int upt, int threads, cudaStream_t s) {
-  return vec ? by_upt<T, QT, true>(p, upt, threads, s) : by_upt<T, QT, false>(p, upt, threads, s);
+arnq_status by_mode(const NormsParams &p, int mode, int upt, int threads, cudaStream_t s) {
+  if (mode == WIDE) return by_upt<T, QT, WIDE>(p, upt, threads, s);
+  if constexpr (QT != 1)
+    if (mode == ONES) return by_upt<T, QT, ONES>(p, upt, threads, s);
+  return by_upt<T, QT, PAIRS>(p, upt, threads, s);
 }
 template <class T>
-arnq_status by_codes(const NormsParams &p, int qt, bool vec, int upt, int threads, cudaStream_t s) {
-  if (qt == 0) return by_vec<T, 0>(p, vec, upt, threads, s);
-  if (qt == 1) return by_vec<T, 1>(p, vec, upt, threads, s);
-  return by_vec<T, kQNone>(p, vec, upt, threads, s);
+arnq_status by_codes(const NormsParams &p, int qt, int mode, int upt, int threads, cudaStream_t s) {
+  if (qt == 0) return by_mode<T, 0>(p, mode, upt, threads, s);
+  if (qt == 1) return by_mode<T, 1>(p, mode, upt, threads, s);
+  return by_mode<T, kQNone>(p, mode, upt, threads, s);
 }
 }  // namespace
 
@@ -62,7 +65,6 @@ extern "C" arnq_status arnq_post_norm_add_rms_norm_dynamic_quant(
   p.out.scale = scale;
   p.out.rows = rows;
   p.out.n = static_cast<int32_t>(n);
-  p.out.units = static_cast<int32_t>(div_up(n, 8));
   p.h = static_cast<const uint16_t *>(h);
   p.x = static_cast<const uint16_t *>(x);
   p.gamma_post = static_cast<const uint16_t *>(gamma_post);
@@ -79,8 +81,10 @@ extern "C" arnq_status arnq_post_norm_add_rms_norm_dynamic_quant(
   int dev = 0, sms = 0, upt = 0, threads = 0;
   st = current_device(&dev, &sms);
   if (st != ARNQ_OK) return st;
-  row_threads(p.out.units, rows > sms, qt == kQNone ? 288 : 384, &upt, &threads);
+  const int mode = vec ? WIDE : n % 2 == 0 ? PAIRS : ONES;
+  p.out.units = units_of(mode, p.out.n);
+  row_threads(p.out.units, mode == WIDE, rows > sms, qt == kQNone ? 288 : 384, &upt, &threads);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return dt == ARNQ_BF16 ? by_codes<Bf16>(p, qt, vec, upt, threads, s)
-                         : by_codes<Fp16>(p, qt, vec, upt, threads, s);
+  return dt == ARNQ_BF16 ? by_codes<Bf16>(p, qt, mode, upt, threads, s)
+                         : by_codes<Fp16>(p, qt, mode, upt, threads, s);
 }

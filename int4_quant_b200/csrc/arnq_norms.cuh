@@ -63,11 +63,11 @@ __device__ __forceinline__ uint16_t x64(uint16_t h, uint16_t x, const uint16_t *
   if (gate) t = __dmul_rn(t, static_cast<double>(Cvt<T>::f1(*gate)));
   return round16<T>(__dadd_rn(static_cast<double>(Cvt<T>::f1(x)), t));
 }
-// The elements of a unit whose halves differ between lo and hi (the bound's two
-// ends), from the unit's inputs h and x; `count` elements exist.
-template <class T>
+// The elements of unit u whose halves differ between lo and hi (the bound's two
+// ends), from the unit's inputs h and x.
+template <class T, int MODE>
 __device__ __noinline__ uint4 settle_x(uint4 lo, uint4 hi, uint4 h, uint4 x, const uint16_t *gamma_post,
-                                       const uint16_t *gate, double inv, int count) {
+                                       const uint16_t *gate, double inv, int u, int n) {
   unsigned m = 0u;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -76,9 +76,9 @@ __device__ __noinline__ uint4 settle_x(uint4 lo, uint4 hi, uint4 h, uint4 x, con
   }
 #pragma unroll 1
   for (; m; m &= m - 1u) {
-    const int j = __ffs(m) - 1;
-    set16(lo, j, j < count ? x64<T>(get16(h, j), get16(x, j), gamma_post + j, gate ? gate + j : nullptr, inv)
-                           : static_cast<uint16_t>(0));
+    const int j = __ffs(m) - 1, c = column<MODE>(u, j);
+    set16(lo, j, c < n ? x64<T>(get16(h, j), get16(x, j), gamma_post + c, gate ? gate + c : nullptr, inv)
+                       : static_cast<uint16_t>(0));
   }
   return lo;
 }
@@ -97,13 +97,14 @@ __device__ __noinline__ double sumsq_cold(const uint16_t *a, const uint16_t *h, 
   return s;
 }
 
-template <class T_, int QT_, bool VEC_, int UPT_, bool FULL_ = false>
+template <class T_, int QT_, int MODE_, int UPT_, bool FULL_ = false>
 struct NormsOp {
   typedef T_ T;
   typedef NormsParams Params;
   static constexpr int QT = QT_, UPT = UPT_, kInputs = 2;
   static constexpr bool kReadsSlots = false;  // after prepare()
-  static constexpr bool FULL = FULL_, VEC = VEC_, STAGED = VEC_ && UPT_ > 0;
+  static constexpr int MODE = MODE_;
+  static constexpr bool FULL = FULL_, STAGED = MODE_ == WIDE && UPT_ > 0;
   static constexpr int kMaxThreads = UPT == 4 ? (QT == kQNone ? 288 : 384) : 1024,
                        kMinCtas = UPT == 4 ? (QT == kQNone ? 3 : 2) : 1;
   struct Keep {
@@ -126,7 +127,7 @@ struct NormsOp {
     float b = 0.f;
     for (int u = tid; u < p.out.units; u += nt) {
       float2 v[4];
-      unpack<T>(load_unit<VEC>(p.beta, 0, u, p.out.n, p.out.n), v);
+      unpack<T>(load_unit<MODE>(p.beta, u, p.out.n), v);
       times(v, p.smooth, u);
       b = abs_top8(v, b);
     }
@@ -136,7 +137,7 @@ struct NormsOp {
   __device__ __forceinline__ void times(float2 v[4], const uint16_t *by, int u) const {
     if (!by) return;
     float2 s[4];
-    unpack<T>(load_unit<VEC>(by, 0, u, p.out.n, p.out.n), s);
+    unpack<T>(load_unit<MODE>(by, u, p.out.n), s);
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = __fmul2_rn(v[k], s[k]);
   }
@@ -152,15 +153,15 @@ struct NormsOp {
     copy16_async(slot + stride, p.x + off);
   }
   __device__ __forceinline__ uint4 get_h(int64_t row, int u, const uint4 *slot) const {
-    return STAGED ? slot[0] : load_unit<VEC>(p.h, row * p.out.n, u, p.out.n, p.out.rows * p.out.n);
+    return STAGED ? slot[0] : load_unit<MODE>(p.h + row * p.out.n, u, p.out.n);
   }
   __device__ __forceinline__ uint4 get_x(int64_t row, int u, const uint4 *slot, int stride) const {
-    return STAGED ? slot[stride] : load_unit<VEC>(p.x, row * p.out.n, u, p.out.n, p.out.rows * p.out.n);
+    return STAGED ? slot[stride] : load_unit<MODE>(p.x + row * p.out.n, u, p.out.n);
   }
   // long rows: x' of a unit after the row's first phases, read back or made again
   __device__ __forceinline__ void x_again(int64_t row, int u, Keep &keep) const {
     if (p.x_out) {
-      unpack<T>(load_unit<VEC>(p.x_out, row * p.out.n, u, p.out.n, p.out.rows * p.out.n), keep.f);
+      unpack<T>(load_unit<MODE>(p.x_out + row * p.out.n, u, p.out.n), keep.f);
     } else {
       unpack<T>(get_h(row, u, nullptr), keep.f);
       make_x(row, u, keep, nullptr, 0);
@@ -172,7 +173,7 @@ struct NormsOp {
     float2 x[4], G[4];
     const uint4 xw = get_x(row, u, slot, stride);
     unpack<T>(xw, x);
-    unpack<T>(load_unit<VEC>(p.gamma_post, 0, u, p.out.n, p.out.n), G);
+    unpack<T>(load_unit<MODE>(p.gamma_post, u, p.out.n), G);
     times(G, gate_row, u);
     const float2 f = make_float2(post.inv, post.inv);
     float2 v[4];
@@ -198,8 +199,8 @@ struct NormsOp {
     }
     uint4 r = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     if (differ)
-      r = settle_x<T>(r, make_uint4(hi[0], hi[1], hi[2], hi[3]), get_h(row, u, slot), xw, p.gamma_post + 8 * u,
-                      gate_row ? gate_row + 8 * u : nullptr, post.inv64, p.out.n - 8 * u);
+      r = settle_x<T, MODE>(r, make_uint4(hi[0], hi[1], hi[2], hi[3]), get_h(row, u, slot), xw, p.gamma_post,
+                            gate_row, post.inv64, u, p.out.n);
     unpack<T>(r, keep.f);
     return r;
   }
@@ -228,7 +229,7 @@ struct NormsOp {
       if (UPT == 0) unpack<T>(get_h(row, u, nullptr), keep[0].f);
       const uint4 x = make_x(row, u, keep[i], slot + i * nt, stride);
       ss += sumsq(keep[i].f);
-      if (p.x_out) store_unit<VEC>(p.x_out + row * p.out.n, u, p.out.n, x);
+      if (p.x_out) store_unit<MODE>(p.x_out + row * p.out.n, u, p.out.n, x);
     });
     ss = block_sum(ss, sm.sum[1], nwarps);
     cold = ss_out_of_range(ss, p.eps);
@@ -244,11 +245,11 @@ struct NormsOp {
   __device__ __forceinline__ bool value(int64_t row, int u, Keep &keep, const uint4 *, int, float2 v[4]) const {
     if (UPT == 0) x_again(row, u, keep);
     float2 G[4], B[4];
-    unpack<T>(load_unit<VEC>(p.gamma, 0, u, p.out.n, p.out.n), G);
+    unpack<T>(load_unit<MODE>(p.gamma, u, p.out.n), G);
     times(G, p.smooth, u);
     const float2 r = make_float2(pre.inv, pre.inv);
     if (p.beta) {
-      unpack<T>(load_unit<VEC>(p.beta, 0, u, p.out.n, p.out.n), B);
+      unpack<T>(load_unit<MODE>(p.beta, u, p.out.n), B);
       times(B, p.smooth, u);
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = __ffma2_rn(__fmul2_rn(keep.f[k], r), G[k], B[k]);

@@ -54,58 +54,97 @@ __device__ __forceinline__ void set16(uint4 &w, int j, uint16_t v) {
   if ((j >> 1) == 3) w.w = (w.w & keep) | put;
 }
 
-// Elements 8u .. 8u+7 of a row of n that starts `at` elements into an array of
-// `count`; zeros past the row's end.  VEC: 16-byte aligned, n a multiple of 8.
-// Otherwise two aligned 16-byte loads around the unit, shifted into place, or,
-// where they would leave the array, one element at a time.
-template <bool VEC>
-__device__ __forceinline__ uint4 load_unit(const uint16_t *array, int64_t at, int u, int n, int64_t count) {
-  const uint16_t *p = array + at + 8 * static_cast<int64_t>(u);
-  if (VEC) return *reinterpret_cast<const uint4 *>(p);
-  const int left = n - 8 * u;  // elements of the unit that exist
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), q = a & ~static_cast<uintptr_t>(15);
-  const uint32_t off = static_cast<uint32_t>(a & 15);
+// A unit is eight elements of a row, held as eight 16-bit halves.  Which ones:
+//   WIDE   8u + j: one 16-byte access (n a multiple of 8, everything aligned)
+//   PAIRS  element pairs 64 apart, the warp's lanes side by side: four 4-byte
+//          (or eight 2-byte) accesses of whole runs (n even)
+//   ONES   elements 32 apart, the lanes side by side (n odd)
+enum : int { WIDE = 0, PAIRS = 1, ONES = 2 };
+template <int MODE>
+__device__ __forceinline__ int column(int u, int j) {
+  if (MODE == WIDE) return 8 * u + j;
+  const int base = (u >> 5) * 256, lane = u & 31;
+  return MODE == PAIRS ? base + (j >> 1) * 64 + 2 * lane + (j & 1) : base + j * 32 + lane;
+}
+__host__ __device__ inline int units_of(int mode, int n) {
+  return mode == WIDE ? n / 8 : (n + 255) / 256 * 32;
+}
+
+// Unit u of a row of n; zeros past the row's end.
+template <int MODE>
+__device__ __forceinline__ uint4 load_unit(const uint16_t *row, int u, int n) {
+  if (MODE == WIDE) return *reinterpret_cast<const uint4 *>(row + 8 * static_cast<int64_t>(u));
+  const int c = column<MODE>(u, 0);
+  const uint16_t *p = row + c;
   uint32_t r[4];
-  if (q >= reinterpret_cast<uintptr_t>(array) &&
-      q + (off ? 32 : 16) <= reinterpret_cast<uintptr_t>(array + count)) {
-    const uint4 lo = *reinterpret_cast<const uint4 *>(q);
-    const uint4 hi = off ? *reinterpret_cast<const uint4 *>(q + 16) : lo;
-    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    if (off & 8) {
+  if (MODE == PAIRS) {
+    const bool words = (reinterpret_cast<uintptr_t>(row) & 3) == 0;  // the same for the whole tensor
 #pragma unroll
-      for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-    }
-    if (off & 4) {
-#pragma unroll
-      for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = __funnelshift_r(w[i], w[i + 1], (off & 2) * 8);
-    if (left < 8) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        r[i] &= (left > 2 * i ? 0xFFFFu : 0u) | (left > 2 * i + 1 ? 0xFFFF0000u : 0u);
+    for (int i = 0; i < 4; ++i) {
+      r[i] = 0u;
+      if (c + 64 * i < n)
+        r[i] = words ? *reinterpret_cast<const uint32_t *>(p + 64 * i)
+                     : p[64 * i] | static_cast<uint32_t>(p[64 * i + 1]) << 16;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t x = left > 2 * i ? p[2 * i] : 0u, y = left > 2 * i + 1 ? p[2 * i + 1] : 0u;
-      r[i] = x | y << 16;
+      const uint32_t lo = c + 64 * i < n ? p[64 * i] : 0u, hi = c + 64 * i + 32 < n ? p[64 * i + 32] : 0u;
+      r[i] = lo | hi << 16;
     }
   }
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-template <bool VEC>
+template <int MODE>
 __device__ __forceinline__ void store_unit(uint16_t *row, int u, int n, const uint4 &w) {
-  if (VEC) {
+  if (MODE == WIDE) {
     *reinterpret_cast<uint4 *>(row + 8 * static_cast<int64_t>(u)) = w;
     return;
   }
-  const int c = 8 * u;
+  const int c = column<MODE>(u, 0);
+  uint16_t *p = row + c;
+  if (MODE == PAIRS && (reinterpret_cast<uintptr_t>(row) & 3) == 0) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (c + j < n) row[c + j] = get16(w, j);
+    for (int i = 0; i < 4; ++i)
+      if (c + 64 * i < n) *reinterpret_cast<uint32_t *>(p + 64 * i) = word_of(w, i);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int d = column<MODE>(u, j) - c;
+    if (c + d < n) p[d] = get16(w, j);
+  }
+}
+
+// Eight codes (bytes, or nibbles in lo) of unit u of the code row.
+template <int MODE, int QT>
+__device__ __forceinline__ void store_codes(uint8_t *row, int u, int n, uint32_t lo, uint32_t hi) {
+  if (MODE == WIDE) {
+    if (QT == 0) reinterpret_cast<uint2 *>(row)[u] = make_uint2(lo, hi);
+    else reinterpret_cast<uint32_t *>(row)[u] = lo;
+    return;
+  }
+  if (QT == 1) {  // (PAIRS) a byte a pair
+    const int c = column<MODE>(u, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + 64 * i < n) row[(c + 64 * i) >> 1] = static_cast<uint8_t>(lo >> (8 * i));
+    return;
+  }
+  const int c = column<MODE>(u, 0);
+  if (MODE == PAIRS && (reinterpret_cast<uintptr_t>(row) & 1) == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + 64 * i < n)
+        *reinterpret_cast<uint16_t *>(row + c + 64 * i) = static_cast<uint16_t>((i < 2 ? lo : hi) >> (16 * (i & 1)));
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int d = column<MODE>(u, j) - c;
+    if (c + d < n) row[c + d] = static_cast<uint8_t>((j < 4 ? lo : hi) >> (8 * (j & 3)));
+  }
 }
 
 template <class T>
@@ -238,7 +277,7 @@ struct RowOut {
   float *scale;
   int64_t rows;
   int32_t n;
-  int32_t units;  // ceil(n / 8)
+  int32_t units;  // of a row
 };
 
 // ------------------------------------------------------------ staging
@@ -261,15 +300,15 @@ __device__ __forceinline__ float rcp_approx(float y) {
   return e;
 }
 
-// Column c's code into row yr, by the eight lanes of unit u (u < 0: none), all
-// of which call it.
+// Column c's code into row yr (nothing for c >= n), by eight lanes, of which an
+// even one and the next have neighbouring columns (INT4); all eight call it.
 template <int QT>
-__device__ __forceinline__ void put_code(uint8_t *yr, int u, int c, int n, int code) {
+__device__ __forceinline__ void put_code(uint8_t *yr, int c, int n, int code) {
   if (QT == 0) {
-    if (u >= 0 && c < n) yr[c] = static_cast<uint8_t>(code);
+    if (c < n) yr[c] = static_cast<uint8_t>(code);
   } else {
     const int up = __shfl_down_sync(0xFFu << (threadIdx.x & 24), code, 1, 8);
-    if (u >= 0 && c < n && (c & 1) == 0) yr[c >> 1] = static_cast<uint8_t>((code & 0xF) | (up << 4));
+    if (c < n && (c & 1) == 0) yr[c >> 1] = static_cast<uint8_t>((code & 0xF) | (up << 4));
   }
 }
 
@@ -286,11 +325,11 @@ __device__ __forceinline__ void settle_rows(Op &op, RowRecord *recs, int count, 
     RowRecord &rec = recs[r];
     op.restore(rec.row, rec.stat);
     const bool all = rec.tops > kMaxCap;
-    const int tops = all ? out.units : rec.tops;
+    const int tops = all ? (n + 7) / 8 : rec.tops;
     double top = 0.0;
 #pragma unroll 1
     for (int i = 0; i < tops; ++i) {
-      const int c = 8 * (all ? i : rec.top[i]) + lane;
+      const int c = all ? 8 * i + lane : column<Op::MODE>(rec.top[i], lane);
       if (c < n) top = fmax(top, fabs(op.value64(rec.row, c)));
     }
     top = group_max_d(top, mask, 8);
@@ -305,18 +344,18 @@ __device__ __forceinline__ void settle_rows(Op &op, RowRecord *recs, int count, 
   for (int i = group;; i += groups) {
     int here = 0;
     for (; r < count; ++r) {
-      here = recs[r].units > kListCap ? out.units : recs[r].units;
+      here = recs[r].units > kListCap ? (n + 7) / 8 : recs[r].units;
       if (i < before + here) break;
       before += here;
     }
     if (r >= count) break;
     const RowRecord &rec = recs[r];
     op.restore(rec.row, rec.stat);
-    const int u = rec.units > kListCap ? i - before : rec.unit[i - before], c = 8 * u + lane;
+    const int c = rec.units > kListCap ? 8 * (i - before) + lane : column<Op::MODE>(rec.unit[i - before], lane);
     const float sc = rec.scale;
     const double in = c < n ? op.value64(rec.row, c) : 0.0;
     __syncwarp(mask);
-    put_code<Op::QT>(out.y + rec.row * (Op::QT == 1 ? n / 2 : n), u, c, n,
+    put_code<Op::QT>(out.y + rec.row * (Op::QT == 1 ? n / 2 : n), c, n,
                      code_exact(in, sc, __double2float_rn(in) * rcp_approx(sc), Q));
   }
   __syncthreads();
@@ -324,7 +363,7 @@ __device__ __forceinline__ void settle_rows(Op &op, RowRecord *recs, int count, 
 }
 
 // Op: struct with
-//   Params, T, VEC (16-byte units), UPT (units per thread held in registers;
+//   Params, T, MODE (the units' shape), UPT (units per thread held in registers;
 //   0: rows longer than that are read again in every phase), FULL (units fill
 //   the threads exactly: no unit is checked, which lets a thread's units
 //   overlap), QT (code type: 0 INT8, 1 INT4, kQNone), STAGED (inputs staged as above), kInputs
@@ -346,7 +385,7 @@ __device__ __forceinline__ void settle_rows(Op &op, RowRecord *recs, int count, 
 template <class Op>
 __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel(const __grid_constant__ typename Op::Params p) {
   constexpr int UPT = Op::UPT, NU = UPT > 0 ? UPT : 1;
-  constexpr bool VEC = Op::VEC;
+  constexpr int MODE = Op::MODE;
   constexpr int Q = Op::QT == 1 ? 7 : 127;
   __shared__ RowSmem sm;
   extern __shared__ uint4 slots[];
@@ -370,12 +409,12 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
       for (int u = tid; u < units; u += nt) f(u, 0);
     }
   };
-  // use(u, c, value64(row, c)) for every column, by whole warps, eight lanes a unit
-  auto each_unit64 = [&](int64_t r, auto &&use) {
+  // use(c, value64(row, c)) for every column, by whole warps (c >= n: none)
+  auto each_column64 = [&](int64_t r, auto &&use) {
 #pragma unroll 1
-    for (int u0 = (tid >> 5) * 4; u0 < units; u0 += nwarps * 4) {
-      const int u = u0 + ((tid & 31) >> 3) < units ? u0 + ((tid & 31) >> 3) : -1, c = 8 * u + (tid & 7);
-      use(u, c, u >= 0 && c < n ? op.value64(r, c) : 0.0);
+    for (int c0 = tid & ~31; c0 < n; c0 += nt) {
+      const int c = c0 + (tid & 31);
+      use(c, c < n ? op.value64(r, c) : 0.0);
     }
   };
   int64_t row = blockIdx.x;
@@ -406,11 +445,11 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) w[k] = Cvt<typename Op::T>::pack(v[i][k].x, v[i][k].y);
-        store_unit<VEC>(yr, u, n, make_uint4(w[0], w[1], w[2], w[3]));
+        store_unit<MODE>(yr, u, n, make_uint4(w[0], w[1], w[2], w[3]));
       });
       if (__syncthreads_or(!sure))  // (a property of the row)
-        each_unit64(row, [&](int u, int c, double in) {
-          if (u >= 0 && c < n) yr[c] = round16<typename Op::T>(in);
+        each_column64(row, [&](int c, double in) {
+          if (c < n) yr[c] = round16<typename Op::T>(in);
         });
       continue;
     }
@@ -432,7 +471,7 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
       if (tid == 0) sm.cand = 0ull;
       __syncthreads();
       unsigned long long best = 0ull;
-      each_unit64(row, [&](int, int, double in) {
+      each_column64(row, [&](int, double in) {
         best = max(best, static_cast<unsigned long long>(__double_as_longlong(fabs(in))));
       });
       if (best) atomicMax(&sm.cand, best);
@@ -441,8 +480,8 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
           div_ieee(__longlong_as_double(static_cast<long long>(sm.cand)), static_cast<double>(Q)));
       const bool finite = sc > 0.f && sc <= 3.402823466e38f;  // else every code is 0
       if (tid == 0) out.scale[row] = sc;
-      each_unit64(row, [&](int u, int c, double in) {
-        put_code<Op::QT>(yr, u, c, n,
+      each_column64(row, [&](int c, double in) {
+        put_code<Op::QT>(yr, c, n,
                          finite && in == in ? code_of_t(div_ieee(in, static_cast<double>(sc)), Q) : 0);
       });
       continue;
@@ -493,16 +532,7 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
         lo = (even & 0x0F0F0F0Fu) | ((odd << 4) & 0xF0F0F0F0u);
         hi = 0u;
       }
-      if (VEC) {
-        if (Op::QT == 0) reinterpret_cast<uint2 *>(yr)[u] = make_uint2(lo, hi);
-        else reinterpret_cast<uint32_t *>(yr)[u] = lo;
-      } else {
-        const int cnt = min(8, n - 8 * u), bytes = Op::QT == 0 ? cnt : cnt / 2;
-        uint8_t *to = yr + static_cast<int64_t>(u) * (Op::QT == 0 ? 8 : 4);
-#pragma unroll
-        for (int j = 0; j < (Op::QT == 0 ? 8 : 4); ++j)
-          if (j < bytes) to[j] = static_cast<uint8_t>((j < 4 ? lo : hi) >> (8 * (j & 3)));
-      }
+      store_codes<MODE, Op::QT>(yr, u, n, lo, hi);
       if (off >= 0.5f - op.coarse(keep[i], inv)) {
         const int at = atomicAdd(&rec.units, 1);
         if (at < kListCap) rec.unit[at] = static_cast<uint16_t>(u);

@@ -32,11 +32,11 @@ inline int kernel_qt(int qdt) {
 // threads for a row of `units`.  Four units a thread where rows outnumber the
 // SMs and max4 such threads hold the row (a row's fixed cost, reductions and barriers, is then shared by few
 // threads); with fewer rows the row's latency counts: the most threads.
-inline void row_threads(int units, bool many, int max4, int *upt, int *threads) {
+inline void row_threads(int units, bool wide, bool many, int max4, int *upt, int *threads) {
   if (many && units <= 4 * max4) *upt = units <= 32 ? 1 : 4;
   else if (units <= 1024) *upt = 1;
-  else if (units <= 2048) *upt = 2;
-  else *upt = 0;
+  else if (wide && units <= 2048) *upt = 2;
+  else *upt = units <= 4 * max4 ? 4 : 0;
   const int per = *upt == 0 ? 2 : *upt;
   int t = static_cast<int>(div_up(div_up(units, per), 32) * 32);
   if (t > 1024) t = 1024;

@@ -106,6 +106,18 @@ def test_norms_many_rows(rows, n):
     check_norms(c, run_norms(c, "int8"), "int8")
 
 
+@pytest.mark.parametrize("qdtype", ["int8", "int4", None])
+@pytest.mark.parametrize("rows,n", [(300, 5002), (170, 258), (40, 9990)])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_rows_of_pairs(rows, n, qdtype, offset):
+    # even lengths that 16-byte loads do not divide, starting on and off 4-byte boundaries
+    c = norms_case(rows, n, "fp16", seed=n, gate_rows=1, beta=True)
+    check_norms(c, run_norms(c, qdtype, offset=offset), qdtype)
+    if qdtype:
+        x, s = glu_case(rows, n, seed=n, smooth=True)
+        check_glu(x, s, "silu", qdtype, offset=offset)
+
+
 @pytest.mark.parametrize("n", [520, 20000])
 def test_norms_in_place(n):
     c = norms_case(6, n, seed=5, gate_rows=1)
