@@ -77,7 +77,16 @@ __device__ __forceinline__ uint4 load_unit(const uint16_t *row, int u, int n) {
   const int c = column<MODE>(u, 0);
   const uint16_t *p = row + c;
   uint32_t r[4];
-  if (MODE == PAIRS) {
+  if ((u >> 5) * 256 + 256 <= n) {  // (the warp's 256 elements all exist)
+    const bool words = MODE == PAIRS && (reinterpret_cast<uintptr_t>(row) & 3) == 0;
+    if (words) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = *reinterpret_cast<const uint32_t *>(p + 64 * i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = p[64 * i] | static_cast<uint32_t>(p[64 * i + (MODE == PAIRS ? 1 : 32)]) << 16;
+    }
+  } else if (MODE == PAIRS) {
     const bool words = (reinterpret_cast<uintptr_t>(row) & 3) == 0;  // the same for the whole tensor
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
