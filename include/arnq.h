@@ -247,9 +247,10 @@ ARNQ_API arnq_status arnq_quant_matmul(const void *x, const float *scale_x, cons
  * Conventions are those of arnq_run: x' is the value an fp64 evaluation gives,
  * rounded once; the x' that was rounded is the one that is normalised; scale
  * and codes are the fp64 evaluation's.  A row whose Rms is 0 (zeros, with
- * eps 0) is normalised to zeros.  A row with a NaN among its inputs gets scale
- * NaN, one with an infinity (and no NaN) scale infinity, both with codes 0.
- * Deterministic; one launch; needs no workspace.
+ * eps 0) is normalised to zeros.  A row whose inputs hold a NaN or an infinity
+ * gets a scale that is NaN or infinite, as the formula has it, and codes 0.
+ * The current device's memory; x_out may be x, no other output may overlap an
+ * input.  Deterministic; one launch; needs no workspace.
  * ARNQ_ERR_ARG: residual_scale not finite, gate_rows < 0 or not dividing rows,
  * or gate_rows == 0 with a gate or > 0 without. */
 ARNQ_API arnq_status arnq_post_norm_add_rms_norm_dynamic_quant(
@@ -270,7 +271,7 @@ typedef enum arnq_activation {
  *   smooth  [n] dtype          optional (NULL = 1)
  *   y       [rows, n] codes, scale [rows] binary32
  * Scale and codes are those of an fp64 evaluation; rows with NaN or infinite
- * values as above.  Deterministic; one launch; needs no workspace.
+ * inputs as above.  Deterministic; one launch; needs no workspace.
  * ARNQ_ERR_ARG: unknown activation. */
 ARNQ_API arnq_status arnq_glu_dynamic_quant(const void *x, const void *smooth, int64_t rows,
                                             int64_t n, arnq_dtype dt, arnq_activation act,

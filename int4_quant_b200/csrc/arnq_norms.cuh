@@ -182,7 +182,7 @@ struct NormsOp {
     for (int k = 0; k < 4; ++k) {
       const float2 hg = __fmul2_rn(keep.f[k], G[k]);
       v[k] = __ffma2_rn(hg, f, x[k]);
-      tmax = abs_max3(hg.x, hg.y, tmax);
+      tmax = abs_max3_nan(hg.x, hg.y, tmax);
     }
     // the unit's largest |h G| serves its eight elements; products below the
     // normal range lose up to 2^-149 each; a cold row has no binary32 bound:
@@ -198,9 +198,10 @@ struct NormsOp {
       differ |= lo[k] ^ hi[k];
     }
     uint4 r = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    if (differ)
-      r = settle_x<T, MODE>(r, make_uint4(hi[0], hi[1], hi[2], hi[3]), get_h(row, u, slot), xw, p.gamma_post,
-                            gate_row, post.inv64, u, p.out.n);
+    const bool beyond = !(tmax <= kHuge);  // a product overflowed (0 times it would be NaN), or is NaN
+    if (differ || beyond)
+      r = settle_x<T, MODE>(r, beyond ? make_uint4(~lo[0], ~lo[1], ~lo[2], ~lo[3]) : make_uint4(hi[0], hi[1], hi[2], hi[3]),
+                            get_h(row, u, slot), xw, p.gamma_post, gate_row, post.inv64, u, p.out.n);
     unpack<T>(r, keep.f);
     return r;
   }

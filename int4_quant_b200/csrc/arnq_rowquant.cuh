@@ -451,12 +451,13 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
       bool sure = true;
       each([&](int u, int i) {
         sure = op.value(row, u, keep[i], slots + i * nt + tid, UPT * nt, v[i]) && sure;
+        sure = sure && abs_top8(v[i], 0.f) <= kHuge;
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) w[k] = Cvt<typename Op::T>::pack(v[i][k].x, v[i][k].y);
         store_unit<MODE>(yr, u, n, make_uint4(w[0], w[1], w[2], w[3]));
       });
-      if (__syncthreads_or(!sure))  // (a property of the row)
+      if (__syncthreads_or(!sure))
         each_column64(row, [&](int c, double in) {
           if (c < n) yr[c] = round16<typename Op::T>(in);
         });

@@ -169,6 +169,36 @@ def test_norms_special_rows(qdtype, n):
         assert not R.codes_of(y[5:7], qdtype).any()
 
 
+@pytest.mark.parametrize("n", [256, 250, 251, 20000])
+def test_norms_special_rows_without_codes(n):
+    c = norms_case(6, n, seed=18, gate_rows=1, smooth=True, beta=True)
+    c["h"][0] = 0
+    c["x"][0] = 0
+    c["h"][1] *= 1e30
+    c["x"][2] *= 1e35
+    c["x"][3] *= 1e-30
+    c["h"][3] *= 1e-30
+    c["x"][4, 3] = float("nan")
+    c["x"][5, 4] = float("inf")
+    y, _, x_out = [t.cpu() if t is not None else None for t in run_norms(c, None, eps=0.0)]
+    sub = {k: (v[:4] if k in ("h", "x") else v) for k, v in c.items()}
+    check_norms(sub, (y[:4], None, x_out[:4]), None, eps=0.0)
+    assert torch.isnan(y[4]).all() and torch.isnan(y[5, 4])
+
+
+@pytest.mark.parametrize("qdtype", ["int8", "int4", None])
+@pytest.mark.parametrize("n", [256, 250, 20000])
+def test_norms_parameter_products_beyond_binary32(qdtype, n):
+    # gamma_post * gate and gamma * smooth overflow a binary32 product where h, x' are zero
+    c = norms_case(4, n, seed=19, gate_rows=1, smooth=True)
+    c["gamma_post"][7], c["gate"][0, 7] = 1e30, 1e30
+    c["gamma"][9], c["smooth"][9] = 3e25, 1e30
+    c["h"][:, 7] = 0
+    c["h"][:, 9] = 0
+    c["x"][:, 9] = 0
+    check_norms(c, run_norms(c, qdtype), qdtype)
+
+
 @pytest.mark.parametrize("alpha", [0.0, 1.0, -0.5, 1e-38, 1e30])
 def test_norms_residual_scale(alpha):
     c = norms_case(4, 264, seed=9, gate_rows=4)
