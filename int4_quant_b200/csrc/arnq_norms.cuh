@@ -192,9 +192,10 @@ struct NormsOp {
     uint32_t lo[4], hi[4], differ = 0u;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float ex = __fmaf_rn(fabsf(v[k].x), kSumError, e), ey = __fmaf_rn(fabsf(v[k].y), kSumError, e);
-      lo[k] = Cvt<T>::pack(v[k].x - ex, v[k].y - ey);
-      hi[k] = Cvt<T>::pack(v[k].x + ex, v[k].y + ey);
+      const float2 bound = make_float2(__fmaf_rn(fabsf(v[k].x), kSumError, e), __fmaf_rn(fabsf(v[k].y), kSumError, e));
+      const float2 a = __ffma2_rn(bound, make_float2(-1.f, -1.f), v[k]), b = __fadd2_rn(v[k], bound);
+      lo[k] = Cvt<T>::pack(a.x, a.y);
+      hi[k] = Cvt<T>::pack(b.x, b.y);
       differ |= lo[k] ^ hi[k];
     }
     uint4 r = make_uint4(lo[0], lo[1], lo[2], lo[3]);

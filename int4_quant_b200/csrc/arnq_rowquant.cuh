@@ -174,18 +174,17 @@ __device__ __forceinline__ uint16_t round16(double v) {
   return static_cast<uint16_t>(Cvt<T>::pack(__uint_as_float(__float_as_uint(z) | odd), 0.f));
 }
 
-// Sum of squares of a unit in fp64.  Each square is exact in binary32 (but for
-// overflow and underflow), which is cheaper than squaring in fp64; adding
-// them in binary32, even four at a time, was seen to move a rounding of x'.
+// Sum of squares of a unit in fp64 (two chains).  Adding the squares in
+// binary32, even four at a time, was seen to move a rounding of x'.
 __device__ __forceinline__ double sumsq(const float2 f[4]) {
-  double s = 0.0;
+  double s = 0.0, t = 0.0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float2 q = __fmul2_rn(f[k], f[k]);
-    s += static_cast<double>(q.x);
-    s += static_cast<double>(q.y);
+    const double a = static_cast<double>(f[k].x), b = static_cast<double>(f[k].y);
+    s = __fma_rn(a, a, s);
+    t = __fma_rn(b, b, t);
   }
-  return s;
+  return s + t;
 }
 
 // ------------------------------------------------------------ block reductions
