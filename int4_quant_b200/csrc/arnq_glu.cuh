@@ -92,8 +92,8 @@ struct GluOp {
     copy16_async(slot, r);
     copy16_async(slot + stride, r + p.out.n);
   }
-  template <class E>
-  __device__ __forceinline__ void prepare(RowSmem &, int64_t, Keep *, const uint4 *, int, E &&, int) {}
+  template <class E, class N>
+  __device__ __forceinline__ void prepare(RowSmem &, int64_t, Keep *, const uint4 *, int, E &&, int, N &&) {}
 
   static __device__ __forceinline__ float2 arg2(float2 g) {
     if (ACT == ACT_SILU) return g;
@@ -150,7 +150,7 @@ struct GluOp {
   static constexpr float kUnit24 = 5.9604644775390625e-8f;  // 2^-24
   static constexpr float kSlope = ACT == ACT_SILU ? 2.f : 6.f;
   // the row's maximum is taken to have z >= -2 (coarse() counts on it)
-  __device__ __forceinline__ bool sure(int64_t row, int u, const float2 v[4], float thr, const uint4 *) const {
+  __device__ __forceinline__ bool sure(int64_t row, int u, const float2 v[4], float thr) const {
     bool ok = true;
 #pragma unroll
     for (int j = 0; j < 8; ++j)

@@ -207,9 +207,9 @@ struct NormsOp {
     return r;
   }
 
-  template <class E>
+  template <class E, class N>
   __device__ __forceinline__ void prepare(RowSmem &sm, int64_t row, Keep *keep, const uint4 *slot, int nt,
-                                          E &&each, int nwarps) {
+                                          E &&each, int nwarps, N &&next) {
     const int stride = UPT * nt;
     find_gate(row);
     // ---- Rms of h
@@ -233,6 +233,8 @@ struct NormsOp {
       ss += sumsq(keep[i].f);
       if (p.x_out) store_unit<MODE>(p.x_out + row * p.out.n, u, p.out.n, x);
     });
+    asm volatile("" : "+d"(ss));  // the slots have been read once ss is there
+    next();
     ss = block_sum(ss, sm.sum[1], nwarps);
     cold = ss_out_of_range(ss, p.eps);
     if (cold) {
@@ -286,7 +288,7 @@ struct NormsOp {
   __device__ __forceinline__ float slack(float M) const {
     return __fmaf_rn(2.f, bmax, M) * 2.384185791015625e-7f;
   }
-  __device__ __forceinline__ bool sure(int64_t, int, const float2[4], float, const uint4 *) const { return true; }
+  __device__ __forceinline__ bool sure(int64_t, int, const float2[4], float) const { return true; }
   // over the scale: that, the scale's own (4, the same) and 5 for the scale's and
   // the quotient's roundings; one more for the bound's
   __device__ __forceinline__ float coarse(const Keep &, float inv) const {

@@ -377,14 +377,15 @@ __device__ __forceinline__ void settle_rows(Op &op, RowRecord *recs, int count, 
 //   overlap), QT (code type: 0 INT8, 1 INT4, kQNone), STAGED (inputs staged as above), kInputs
 //   (tensors staged), Keep (what a unit keeps besides its values)
 //   stage(row, u, slot, stride)     issues the copies of a unit
-//   prepare(...)                    the row's statistics
+//   prepare(..., next)              the row's statistics; calls next() when the
+//                                   thread's slots have been read, unless
+//                                   kReadsSlots
 //   value(row, u, keep, ..., v)     a unit's binary32 values; returns false
 //                                   where they have no error bound
 //   value64(row, c)                 one value in fp64, from memory
-//   kReadsSlots                     value() reads the slots too, not prepare()
-//                                   alone: the next row is staged later
+//   kReadsSlots                     value() reads the slots, not prepare()
 //   slack(M)                        bound on |value - value64| over the row
-//   sure(row, u, v, thr, slot)      whether the values >= thr of a unit are as
+//   sure(row, u, v, thr)            whether the values >= thr of a unit are as
 //                                   near their fp64 values as coarse() takes the
 //                                   row's maximum to be
 //   coarse(keep, inv)               bound on the error of a unit's quotients, that
@@ -442,8 +443,7 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
     typename Op::Keep keep[NU];
     float2 v[NU][4];
     if (Op::STAGED) copies_wait();
-    op.prepare(sm, row, keep, slots + tid, nt, each, nwarps);
-    if (!Op::kReadsSlots) stage(row + gridDim.x);  // prepare() has read them, behind a barrier
+    op.prepare(sm, row, keep, slots + tid, nt, each, nwarps, [&]() { stage(row + gridDim.x); });
 
     if (Op::QT == kQNone) {
       uint16_t *yr = reinterpret_cast<uint16_t *>(out.y) + row * n;
@@ -469,6 +469,12 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
       if (!op.value(row, u, keep[i], slots + i * nt + tid, UPT * nt, v[i])) top32 = __int_as_float(0x7F800000);
       top32 = abs_top8(v[i], top32);
     });
+    if (Op::kReadsSlots) {
+      // the thread's slots have been read once top32 is there: the next row's
+      // copies into them may go out
+      asm volatile("" : "+f"(top32));
+      stage(row + gridDim.x);
+    }
     const float M = block_max(top32, sm.top[parity], nwarps);
     RowRecord &rec = sm.rec[records];
     const int64_t code_bytes = Op::QT == 1 ? n / 2 : n;
@@ -476,7 +482,6 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
     const bool wide = !(M >= kTiny && M <= kHuge);
     if (wide) {
       // ---- the whole row in fp64
-      if (Op::kReadsSlots) stage(row + gridDim.x);
       if (tid == 0) sm.cand = 0ull;
       __syncthreads();
       unsigned long long best = 0ull;
@@ -501,11 +506,10 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
       each([&](int u, int i) {
         if (UPT == 0) op.value(row, u, keep[i], slots, 0, v[i]);
         if (abs_max8(v[i]) < M - 2.f * op.slack(M)) return;
-        const int at = atomicAdd(&rec.tops, op.sure(row, u, v[i], M - 2.f * op.slack(M), slots + i * nt + tid) ? 1 : kMaxCap + 1);
+        const int at = atomicAdd(&rec.tops, op.sure(row, u, v[i], M - 2.f * op.slack(M)) ? 1 : kMaxCap + 1);
         if (at < kMaxCap) rec.top[at] = static_cast<uint16_t>(u);
       });
     }
-    if (Op::kReadsSlots) stage(row + gridDim.x);  // this row's slots have been read, behind a barrier
     if (tid == 0) {
       op.save(rec.stat);
       rec.row = row;
