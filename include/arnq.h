@@ -17,6 +17,11 @@
  * rules of its "Constraints" section.  The no-add form is the page
  * "aclnnRmsNormDynamicQuant", formula section.
  *
+ * Around it: the product of INT8 codes with token and channel scales
+ * (arnq_quant_matmul), the norms around a block's residual and the gated
+ * activation, both with the same quantization (further down; what this header
+ * says of ownership, errors and launches holds for them too).
+ *
  * Numerical conventions (the pages leave these open; the library fixes them):
  *   - x1 + x2 is a binary32 add rounded once more, to nearest even, to the
  *     input dtype; that rounded x is written as xOut AND is the x that is

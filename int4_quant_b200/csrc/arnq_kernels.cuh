@@ -179,7 +179,6 @@ struct Fp16 {};
 
 template <class T> struct Cvt;
 template <> struct Cvt<Bf16> {
-  static constexpr int kBits = 8;  // of the significand
   // two packed bf16 -> two floats (exact: a bf16 is the top half of a binary32)
   static __device__ __forceinline__ float2 f2(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
@@ -205,7 +204,6 @@ template <> struct Cvt<Bf16> {
   }
 };
 template <> struct Cvt<Fp16> {
-  static constexpr int kBits = 11;
   static __device__ __forceinline__ float2 f2(uint32_t w) {
     __half2 h;
     memcpy(&h, &w, 4);

@@ -17,6 +17,10 @@
 
 namespace arnq {
 
+// h * (gamma_post * gate) is exact in binary32 for bf16: 8 + 16 bits
+template <class T> constexpr bool kExactProducts = false;
+template <> constexpr bool kExactProducts<Bf16> = true;
+
 struct NormsParams {
   RowOut out;
   const uint16_t *h, *x, *gamma_post, *gate, *gamma, *beta, *smooth;
@@ -113,7 +117,7 @@ struct NormsOp {
   // Error of v = x + (h G) f in units of 2^-24: the factor f one of |h G f|, the
   // product h G none in bf16 (8 + 16 bits) and one in fp16 (11 + 22), the
   // fused multiply-add one of |v|; and the bound's own roundings (v +- e).
-  static constexpr float kFactorError = (Cvt<T>::kBits == 8 ? 1.25f : 2.25f) * 5.9604644775390625e-8f;
+  static constexpr float kFactorError = (kExactProducts<T> ? 1.25f : 2.25f) * 5.9604644775390625e-8f;
   static constexpr float kSumError = 2.25f * 5.9604644775390625e-8f;
   const Params &p;
   float bmax;  // max |beta * smooth|
