@@ -227,6 +227,34 @@ ARNQ_API arnq_status arnq_quant_matmul(const void *x, const float *scale_x, cons
                                        int64_t k, arnq_dtype out_dt, void *y, void *workspace,
                                        size_t workspace_bytes, void *stream);
 
+/* How a product is launched; zero fields mean "choose" (for tuning and testing).
+ * Every plan gives the same bits. */
+typedef enum arnq_matmul_kernel {
+  ARNQ_MATMUL_AUTO = 0,
+  ARNQ_MATMUL_SPLIT = 1, /* few tokens: K shared over a cluster                        */
+  ARNQ_MATMUL_PAIR = 2   /* many tokens: tiles of CTA pairs; k and both code pointers
+                            multiples of 16                                          */
+} arnq_matmul_kernel;
+typedef struct arnq_matmul_plan {
+  int32_t kernel;          /* arnq_matmul_kernel                                       */
+  int32_t tokens;          /* split kernel: tokens of a tile, a multiple of 16 up to 256 */
+  int32_t split;           /* split kernel: CTAs sharing a tile's K: 1, 2, 4 or 8, at most
+                              one for each 128 codes of it                            */
+  int32_t wait_limit_us;   /* bounded device waits give up after this many us; 0 = 1 s  */
+  int32_t test_hold_bytes; /* testing only: bytes (at most 65536) that the first stage's
+                              barriers expect beside its copies, so that the waits run out
+                              and the call records ARNQ_ERR_DEVICE_TIMEOUT; its output
+                              is then not valid; 0 in normal use                       */
+} arnq_matmul_plan;
+
+/* arnq_quant_matmul with an explicit plan; ARNQ_ERR_PLAN if it cannot run this
+ * problem. */
+ARNQ_API arnq_status arnq_quant_matmul_planned(const void *x, const float *scale_x, const void *w,
+                                               const float *scale_w, const void *bias, int64_t m,
+                                               int64_t n, int64_t k, arnq_dtype out_dt, void *y,
+                                               void *workspace, size_t workspace_bytes, void *stream,
+                                               const arnq_matmul_plan *plan);
+
 /* The norms around a block's residual, fused: the block's output h is
  * normalised, gated, scaled and added to the residual stream x, and the sum is
  * normalised for the next block and quantized:

@@ -38,6 +38,7 @@ ARNQ_BF16, ARNQ_FP16, ARNQ_FP32 = 0, 1, 2
 ARNQ_INT8, ARNQ_INT4, ARNQ_INT4_INT32 = 0, 1, 2
 ARNQ_NO_CODES = 16
 ARNQ_SILU, ARNQ_GELU_TANH = 0, 1
+ARNQ_MATMUL_AUTO, ARNQ_MATMUL_SPLIT, ARNQ_MATMUL_PAIR = 0, 1, 2
 ARNQ_MASK_ABSENT = -1
 ARNQ_MASK_Y1, ARNQ_MASK_Y2 = 1, 2
 ARNQ_MAX_N = 131072
@@ -55,6 +56,11 @@ class arnq_plan(ctypes.Structure):
 
     def as_dict(self):
         return {f: getattr(self, f) for f, _ in self._fields_}
+
+
+class arnq_matmul_plan(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in
+                ("kernel", "tokens", "split", "wait_limit_us", "test_hold_bytes")]
 
 
 class arnq_workspace_status(ctypes.Structure):
@@ -89,6 +95,8 @@ _SIGS = {
     "arnq_run_static_scratch": ([_p, _p, _p, _p, _p, _p, _i64, _i64, _i32, _f32, _i32, _i32, _p, _p,
                                  _p, _p, _p, _p], _i32),
     "arnq_quant_matmul": ([_p, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _p, _sz, _p], _i32),
+    "arnq_quant_matmul_planned": ([_p, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _p, _sz, _p, _p],
+                                  _i32),
     "arnq_post_norm_add_rms_norm_dynamic_quant": (
         [_p, _p, _p, _p, _i64, _f32, _p, _p, _p, _i64, _i64, _i32, _f32, _f32, _i32, _p, _p, _p,
          _p], _i32),
@@ -241,3 +249,11 @@ def arnq_quant_matmul(x, scale_x, w, scale_w, bias, m, n, k, out_dt, y, workspac
     return lib().arnq_quant_matmul(_ptr(x), _ptr(scale_x), _ptr(w), _ptr(scale_w), _ptr(bias),
                                    int(m), int(n), int(k), int(out_dt), _ptr(y), _ptr(workspace),
                                    int(workspace_bytes), _stream(stream))
+
+
+def arnq_quant_matmul_planned(x, scale_x, w, scale_w, bias, m, n, k, out_dt, y, workspace,
+                              workspace_bytes, stream, plan: arnq_matmul_plan) -> int:
+    return lib().arnq_quant_matmul_planned(
+        _ptr(x), _ptr(scale_x), _ptr(w), _ptr(scale_w), _ptr(bias), int(m), int(n), int(k),
+        int(out_dt), _ptr(y), _ptr(workspace), int(workspace_bytes), _stream(stream),
+        ctypes.addressof(plan))

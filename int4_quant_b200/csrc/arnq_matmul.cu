@@ -89,16 +89,19 @@ double split_slots(int split, int per_sm, int sms) {
   return part * per_sm * sms;
 }
 
-SplitPlan plan_split(const MatmulParams &p, bool plain, int sms) {
+// want: requested tile of tokens and split (0: choose)
+SplitPlan plan_split(const MatmulParams &p, bool plain, int sms, int want_tokens, int want_split) {
   SplitPlan best = {};
   const int chunks = static_cast<int>(div_up(p.k, kTileK));
   const int64_t least = div_up(p.m, 256);  // token tiles; more of them spread a small product
   for (int64_t token_tiles = least; token_tiles <= 4 * least; token_tiles *= 2) {
-    const int tokens = static_cast<int>(div_up(div_up(p.m, token_tiles), 16) * 16);
-    if (token_tiles > least && tokens < 32) break;
+    const int tokens = want_tokens ? want_tokens : static_cast<int>(div_up(div_up(p.m, token_tiles), 16) * 16);
+    if (token_tiles > least && (tokens < 32 || want_tokens)) break;
     const int64_t tiles = div_up(p.n, 128) * div_up(p.m, tokens);
     const int stage = 16384 + tokens * 128;
-    for (int split = 1; split <= 8 && (split == 1 || chunks >= (plain ? 1 : 2) * split); split *= 2) {
+    for (int split = 1; split <= 8 && (split == 1 || split == want_split || chunks >= (plain ? 1 : 2) * split);
+         split *= 2) {
+      if (want_split && split != want_split) continue;
       const int mine = static_cast<int>(div_up(chunks, split));
       // two CTAs an SM where at least three stages (or all there are) fit half of it
       int stages = (kSmemLimit / 2 - kStatic - 1024) / stage, per_sm = 2;
@@ -174,6 +177,18 @@ extern "C" arnq_status arnq_quant_matmul(const void *x, const float *scale_x, co
                                          const float *scale_w, const void *bias, int64_t m, int64_t n,
                                          int64_t k, arnq_dtype out_dt, void *y, void *workspace,
                                          size_t workspace_bytes, void *stream) {
+  arnq_matmul_plan plan;
+  std::memset(&plan, 0, sizeof plan);
+  return arnq_quant_matmul_planned(x, scale_x, w, scale_w, bias, m, n, k, out_dt, y, workspace,
+                                   workspace_bytes, stream, &plan);
+}
+
+extern "C" arnq_status arnq_quant_matmul_planned(const void *x, const float *scale_x, const void *w,
+                                                 const float *scale_w, const void *bias, int64_t m,
+                                                 int64_t n, int64_t k, arnq_dtype out_dt, void *y,
+                                                 void *workspace, size_t workspace_bytes, void *stream,
+                                                 const arnq_matmul_plan *plan) {
+  if (!plan) return ARNQ_ERR_NULL_PTR;
   if (out_dt != ARNQ_BF16 && out_dt != ARNQ_FP16 && out_dt != ARNQ_FP32) return ARNQ_ERR_DTYPE;
   if (m < 0 || n < 0 || k < 0 || m > INT32_MAX || n > ARNQ_MAX_N || k > ARNQ_MAX_K) return ARNQ_ERR_SHAPE;
   if (m == 0 || n == 0 || k == 0) return ARNQ_ERR_EMPTY;
@@ -183,6 +198,14 @@ extern "C" arnq_status arnq_quant_matmul(const void *x, const float *scale_x, co
     return ARNQ_ERR_ALIGN;
   if (!workspace || workspace_bytes < static_cast<size_t>(kStatusBytes)) return ARNQ_ERR_WORKSPACE;
   if (!is_aligned(workspace, 8)) return ARNQ_ERR_ALIGN;
+  const bool plain = k % 16 != 0 || !is_aligned(x, 16) || !is_aligned(w, 16);
+  const arnq_matmul_plan &q = *plan;
+  if (q.kernel < 0 || q.kernel > ARNQ_MATMUL_PAIR || (q.kernel == ARNQ_MATMUL_PAIR && plain) ||
+      q.tokens < 0 || q.tokens > 256 || q.tokens % 16 != 0 ||
+      (q.split != 0 && q.split != 1 && q.split != 2 && q.split != 4 && q.split != 8) ||
+      static_cast<int64_t>(q.split) > div_up(k, kTileK) || q.wait_limit_us < 0 || q.test_hold_bytes < 0 ||
+      q.test_hold_bytes > 65536 || (q.test_hold_bytes > 0 && plain))
+    return ARNQ_ERR_PLAN;
   int dev = 0, sms = 0;
   arnq_status st = current_device(&dev, &sms);
   if (st != ARNQ_OK) return st;
@@ -200,16 +223,17 @@ extern "C" arnq_status arnq_quant_matmul(const void *x, const float *scale_x, co
   p.k = k;
   p.out = static_cast<int32_t>(out_dt);
   p.vec_out = n % 4 == 0 && is_aligned(y, 4 * esz) ? 1 : 0;
-  p.wait_limit_ns = kWaitLimitNs;
-  const bool plain = k % 16 != 0 || !is_aligned(x, 16) || !is_aligned(w, 16);
+  p.wait_limit_ns = q.wait_limit_us > 0 ? static_cast<uint64_t>(q.wait_limit_us) * 1000ull
+                                        : static_cast<uint64_t>(kWaitLimitNs);
+  p.test_hold = static_cast<uint32_t>(q.test_hold_bytes);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const SplitPlan plan = plan_split(p, plain, sms);
-  if (!plain) {
+  const SplitPlan split = plan_split(p, plain, sms, q.tokens, q.split);
+  if (!plain && q.kernel != ARNQ_MATMUL_SPLIT) {
     int pairs = 0;
     st = resident_clusters(reinterpret_cast<const void *>(matmul_pair_kernel), dev, kPairThreads, kPairSmem, 2,
                            &pairs);
     if (st != ARNQ_OK) return st;
-    if (pair_us(p, pairs) < plan.us) return launch_pair(p, pairs, cs);
+    if (q.kernel == ARNQ_MATMUL_PAIR || pair_us(p, pairs) < split.us) return launch_pair(p, pairs, cs);
   }
-  return launch_split(p, plan, plain, dev, cs);
+  return launch_split(p, split, plain, dev, cs);
 }

@@ -32,6 +32,7 @@ struct MatmulParams {
   int32_t stages;
   uint32_t tmem_cols;
   uint64_t wait_limit_ns;
+  uint32_t test_hold;  // testing only: bytes the first stage waits for in vain
 };
 
 __device__ __forceinline__ void report_timeout(int32_t *status) {
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(PLAIN ? kPlainThreads : kSplitThreads)
         const int s = i % stages;
         if (i >= stages && !wait(&empty[s], ((i / stages) & 1) ^ 1)) break;
         const uint32_t bar = smem_addr(&full[s]), at = base + s * stage_bytes;
-        mbar_arrive_expect_tx(bar, stage_bytes);
+        mbar_arrive_expect_tx(bar, stage_bytes + (i == 0 ? p.test_hold : 0u));
         tma_2d(at, &p.map_w, kc * kTileK, static_cast<int>(c0), bar);
         tma_2d(at + 16384u, &p.map_x, kc * kTileK, static_cast<int>(t0), bar);
       }
@@ -435,7 +436,8 @@ __global__ void __launch_bounds__(kPairThreads) matmul_pair_kernel(const __grid_
             ok = false;
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(smem_addr(&full[s]), 2 * kPairStageBytes);
+          if (rank == 0)
+            mbar_arrive_expect_tx(smem_addr(&full[s]), 2 * kPairStageBytes + (filled == 0 ? p.test_hold : 0u));
           const uint32_t bar = full0 + 8 * s, at = base + s * kPairStageBytes;
           tma_2d_pair(at, &p.map_x, kc * kTileK, tx, bar);
           tma_2d_pair(at + 16384, &p.map_w, kc * kTileK, cw, bar);

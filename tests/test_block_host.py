@@ -130,6 +130,27 @@ def test_matmul_refusals(kw, expect):
     assert matmul(**kw) == expect
 
 
+@pytest.mark.parametrize("kw,k,expect", [
+    (dict(kernel=3), 256, A.ARNQ_ERR_PLAN),
+    (dict(kernel=-1), 256, A.ARNQ_ERR_PLAN),
+    (dict(kernel=A.ARNQ_MATMUL_PAIR), 250, A.ARNQ_ERR_PLAN),
+    (dict(tokens=24), 256, A.ARNQ_ERR_PLAN),
+    (dict(tokens=272), 256, A.ARNQ_ERR_PLAN),
+    (dict(split=3), 256, A.ARNQ_ERR_PLAN),
+    (dict(split=16), 4096, A.ARNQ_ERR_PLAN),
+    (dict(split=4), 256, A.ARNQ_ERR_PLAN),
+    (dict(wait_limit_us=-1), 256, A.ARNQ_ERR_PLAN),
+    (dict(test_hold_bytes=65537), 256, A.ARNQ_ERR_PLAN),
+    (dict(test_hold_bytes=16), 250, A.ARNQ_ERR_PLAN),
+])
+def test_matmul_plan_refusals(kw, k, expect):
+    p = A.arnq_matmul_plan()
+    for name, v in kw.items():
+        setattr(p, name, v)
+    assert A.arnq_quant_matmul_planned(P["x"], P["sc"], P["w"], P["sw"], None, 8, 64, k, A.ARNQ_BF16,
+                                       P["y"], P["ws"], 256, None, p) == expect
+
+
 def test_torch_calls_refuse_cpu_tensors():
     codes = torch.zeros(4, 64, dtype=torch.int8)
     with pytest.raises(ValueError):

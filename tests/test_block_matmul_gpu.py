@@ -231,3 +231,55 @@ def test_many_tokens_leaves_neighbours_alone():
 def test_more_tiles_than_pairs(m, n, k, out):
     # several tiles for each pair of CTAs: two at a time, singles behind them, odd rows of tiles
     run(m, n, k, out, out == torch.float32, seed=m)
+
+
+def planned(c, ws=None, **kw):
+    x, sx, w, sw, b = c
+    p = A.arnq_matmul_plan()
+    for name, v in kw.items():
+        setattr(p, name, v)
+    y = torch.zeros(x.shape[0], w.shape[0], dtype=torch.float32, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda") if ws is None else ws
+    st = A.arnq_quant_matmul_planned(x, sx, w, sw, b, x.shape[0], w.shape[0], x.shape[1], A.ARNQ_FP32, y,
+                                     ws, 256, torch.cuda.current_stream(), p)
+    assert st == A.ARNQ_OK, A.arnq_status_string(st)
+    torch.cuda.synchronize()
+    return y, lib.workspace_status(ws)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 128, 1024), (100, 300, 1040), (300, 520, 2064), (513, 776, 1024)])
+def test_plans_give_the_same_bits(m, n, k):
+    c = case(m, n, k, torch.float32, seed=m)
+    ref, status = planned(c)
+    check(*c, ref)
+    assert status[0] == 0
+    for kw in (dict(kernel=2), dict(kernel=1), dict(kernel=1, split=1), dict(kernel=1, split=2, tokens=16),
+               dict(kernel=1, split=4, tokens=64), dict(kernel=1, split=8, tokens=256)):
+        y, status = planned(c, **kw)
+        assert torch.equal(ref, y) and status[0] == 0, kw
+
+
+def test_two_streams_at_once():
+    # both kernels side by side, again and again: SMs, TMEM and shared memory shared between them
+    a, b = case(1200, 1024, 1024, seed=1), case(16, 2048, 2048, seed=2)
+    ra, rb = lib.quant_matmul(*a[:4]), lib.quant_matmul(*b[:4])
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    ya = [lib.quant_matmul(*a[:4], stream=s1) if i % 2 else lib.quant_matmul(*b[:4], stream=s1) for i in range(40)]
+    yb = [lib.quant_matmul(*b[:4], stream=s2.cuda_stream) if i % 2 else
+          lib.quant_matmul(*a[:4], stream=s2.cuda_stream) for i in range(40)]
+    torch.cuda.synchronize()
+    for i in range(40):
+        assert torch.equal(ya[i], ra if i % 2 else rb) and torch.equal(yb[i], rb if i % 2 else ra)
+
+
+@pytest.mark.parametrize("kw", [dict(kernel=1, split=1), dict(kernel=1, split=4), dict(kernel=2)])
+def test_a_wait_that_runs_out_is_reported(kw):
+    c = case(300, 512, 4096, seed=3)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    _, status = planned(c, ws, wait_limit_us=2000, test_hold_bytes=64, **kw)
+    assert status == (A.ARNQ_ERR_DEVICE_TIMEOUT, -1)
+    # the context and the kernels work on
+    y, status = planned(c, **kw)
+    check(*c, y)
+    assert status[0] == 0
