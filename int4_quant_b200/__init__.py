@@ -186,13 +186,17 @@ class _Torch:
 
     def __init__(self):
         import torch
-        self.empty_like, self.empty_strided = torch.empty_like, torch.empty_strided
+        try:  # torch's own shortcut: a new tensor on the current device in half the time
+            self.empty = torch._C._dynamo.guards._empty_strided_cuda
+        except AttributeError:
+            self.empty = lambda shape, strides, dtype: torch.empty_strided(
+                shape, strides, dtype=dtype, device="cuda")
         self.Tensor = torch.Tensor
         self.int8, self.uint8, self.int32 = torch.int8, torch.uint8, torch.int32
         self.float32, self.bfloat16 = torch.float32, torch.bfloat16
         self.dt = {torch.bfloat16: _abi.ARNQ_BF16, torch.float16: _abi.ARNQ_FP16}
         self.out = {**self.dt, torch.float32: _abi.ARNQ_FP32}
-        self.current_device = torch.cuda.current_device
+        self.current_device = torch._C._cuda_getDevice
         # the current stream's handle without building a Stream object
         self.raw_stream = torch._C._cuda_getCurrentRawStream
         self.cuda = torch.cuda
@@ -215,63 +219,67 @@ def _codes_of(T, shape, n, qdtype):
     return _codes_like(tuple(shape[:-1]), n, qdtype)
 
 
-def _operand(t, name, device, dtype, shape=None):
-    """Checks a tensor: CUDA, contiguous, on `device`, of `dtype` (and shape)."""
+def _operand(t, name, index, dtype, shape=None):
+    """Address of a tensor, checked: CUDA device `index`, contiguous, of `dtype`
+    (and shape)."""
     try:
-        if (t.dtype is dtype and t.device == device and t.is_contiguous() and
+        if (t.dtype is dtype and t.get_device() == index and t.is_contiguous() and
                 (shape is None or t.shape == shape)):
             return t.data_ptr()
     except AttributeError:
         pass
     _check(t, name, dtype)
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
     raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _on_stream(call, device, stream):
-    """call(handle of the stream to launch on), with `device` and that stream
+def _on_stream(call, index, stream):
+    """call(handle of the stream to launch on), with device `index` and that stream
     current: outputs allocated inside belong to the stream they are made on."""
-    T = _torch()
+    T = _torch_cache
     if stream is None:
-        if T.current_device() == device.index:
-            return call(T.raw_stream(device.index))
-        with T.cuda.device(device):
-            return call(T.raw_stream(device.index))
+        if T.current_device() == index:
+            return call(T.raw_stream(index))
+        with T.cuda.device(index):
+            return call(T.raw_stream(index))
     if isinstance(stream, int):
-        stream = T.cuda.ExternalStream(stream, device=device)
-    if stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, not on {device}")
+        stream = T.cuda.ExternalStream(stream, device=index)
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, not on cuda:{index}")
     with T.cuda.stream(stream):  # (the device too)
         return call(stream.cuda_stream)
 
 
-def _output(given, name, x, shape, dtype):
-    """An output and its address: the tensor given (checked), or a new one
-    beside x (by the cheapest of torch's ways to make it)."""
+def _output(given, name, index, shape, dtype):
+    """An output and its address: the tensor given (checked) or a new one on the
+    current device."""
     if given is not None:
-        return given, _operand(given, name, x.device, dtype, shape)
-    T = _torch()
-    if shape is x.shape or shape == x.shape:
-        t = T.empty_like(x, dtype=dtype)
-    elif len(shape) == 2:
-        t = T.empty_strided(shape, (shape[1], 1), dtype=dtype, device=x.device)
-    elif len(shape) == 1:
-        t = T.empty_strided(shape, (1,), dtype=dtype, device=x.device)
+        return given, _operand(given, name, index, dtype, shape)
+    d = len(shape)
+    if d == 1:
+        strides = (1,)
+    elif d == 2:
+        strides = (shape[1], 1)
     else:
-        t = x.new_empty(shape, dtype=dtype)
+        strides, step = [], 1
+        for v in reversed(shape):
+            strides.append(step)
+            step *= v
+        strides = tuple(reversed(strides))
+    t = _torch_cache.empty(tuple(shape), strides, dtype)
     return t, t.data_ptr()
 
 
 _status_blocks = {}
 
 
-def _status_block(device, stream: int) -> int:
+def _status_block(index: int, stream: int) -> int:
     """Address of the workspace of calls that only need the status block."""
-    key = (device.index, stream)
+    key = (index, stream)
     kept = _status_blocks.get(key)
     if kept is None:
-        ws = workspace(device, _abi.ARNQ_WORKSPACE_BYTES, stream)
+        ws = workspace(f"cuda:{index}", _abi.ARNQ_WORKSPACE_BYTES, stream)
         kept = _status_blocks[key] = (ws.data_ptr(), ws)
     return kept[0]
 
@@ -286,9 +294,9 @@ def quant_matmul(x, scale_x, w, scale_w, bias=None, *, out_dtype=None, stream=No
     bias: [n] of the output dtype.  out_dtype: torch.bfloat16 (the default),
     float16 or float32; `out` may pass y [..., n] preallocated.
     """
-    T = _torch()
+    T = _torch_cache or _torch()
     _check(x, "x", T.int8)
-    device, shape = x.device, x.shape
+    device, shape = x.get_device(), x.shape
     if out_dtype is None:
         out_dtype = T.bfloat16
     code = T.out.get(out_dtype)
@@ -307,8 +315,8 @@ def quant_matmul(x, scale_x, w, scale_w, bias=None, *, out_dtype=None, stream=No
     oshape = (*lead, n)
 
     def call(s):
-        y, py = _output(out, "out", x, oshape, out_dtype)
-        st = _abi.lib().arnq_quant_matmul(
+        y, py = _output(out, "out", device, oshape, out_dtype)
+        st = (_abi._lib or _abi.lib()).arnq_quant_matmul(
             x.data_ptr(), psx, pw, psw, pb, x.numel() // k if k else 0, n, k, code, py,
             _status_block(device, s), _abi.ARNQ_WORKSPACE_BYTES, s)
         if st != _abi.ARNQ_OK:
@@ -340,9 +348,9 @@ def post_norm_add_rms_norm_dynamic_quant(h, x, gamma_post, gamma, beta=None, gat
     inputs' dtype and scale None.  eps_post defaults to eps.  `out` may pass
     preallocated tensors under the keys y, scale, x_out; x_out may be x.
     """
-    T = _torch()
+    T = _torch_cache or _torch()
     _check(x, "x")
-    dt, device, shape = x.dtype, x.device, x.shape
+    dt, device, shape = x.dtype, x.get_device(), x.shape
     code = T.dt.get(dt)
     if code is None:
         raise ValueError(f"unsupported dtype {dt}")
@@ -368,12 +376,12 @@ def post_norm_add_rms_norm_dynamic_quant(h, x, gamma_post, gamma, beta=None, gat
     given = out or {}
 
     def call(s):
-        y, py = _output(given.get("y"), "y", x, cshape, cdt)
+        y, py = _output(given.get("y"), "y", device, cshape, cdt)
         scale, psc = None, None
         if qdtype is not None:
-            scale, psc = _output(given.get("scale"), "scale", x, lead, T.float32)
-        xo, pxo = _output(given.get("x_out"), "x_out", x, shape, dt)
-        st = _abi.lib().arnq_post_norm_add_rms_norm_dynamic_quant(
+            scale, psc = _output(given.get("scale"), "scale", device, lead, T.float32)
+        xo, pxo = _output(given.get("x_out"), "x_out", device, shape, dt)
+        st = (_abi._lib or _abi.lib()).arnq_post_norm_add_rms_norm_dynamic_quant(
             ph, x.data_ptr(), pgp, pgate, gate_rows, residual_scale, pg, pb, ps,
             x.numel() // n if n else 0, n, code, eps if eps_post is None else eps_post, eps, q,
             py, psc, pxo, s)
@@ -395,9 +403,9 @@ def glu_dynamic_quant(x, smooth=None, *, activation: str = "silu", qdtype: str =
     x: [..., 2n] bf16 or fp16; smooth: [n] same dtype; activation "silu" or
     "gelu_tanh".  Returns (y, scale); `out` may pass them preallocated.
     """
-    T = _torch()
+    T = _torch_cache or _torch()
     _check(x, "x")
-    dt, device, shape = x.dtype, x.device, x.shape
+    dt, device, shape = x.dtype, x.get_device(), x.shape
     code = T.dt.get(dt)
     if code is None:
         raise ValueError(f"unsupported dtype {dt}")
@@ -412,9 +420,9 @@ def glu_dynamic_quant(x, smooth=None, *, activation: str = "silu", qdtype: str =
     given = out or {}
 
     def call(s):
-        y, py = _output(given.get("y"), "y", x, cshape, cdt)
-        scale, psc = _output(given.get("scale"), "scale", x, lead, T.float32)
-        st = _abi.lib().arnq_glu_dynamic_quant(
+        y, py = _output(given.get("y"), "y", device, cshape, cdt)
+        scale, psc = _output(given.get("scale"), "scale", device, lead, T.float32)
+        st = (_abi._lib or _abi.lib()).arnq_glu_dynamic_quant(
             x.data_ptr(), ps, x.numel() // (2 * n) if n else 0, n, code, act, _QDT[qdtype], py, psc,
             s)
         if st != _abi.ARNQ_OK:
