@@ -333,7 +333,8 @@ __global__ void __launch_bounds__(PLAIN ? kPlainThreads : kSplitThreads)
       }
     }
   }
-  cluster.sync();  // nobody leaves while its partial sums are being read
+  __syncwarp();
+  cluster_part();  // nobody leaves while its partial sums are being read
 }
 
 // ------------------------------------------------------------ many tokens
@@ -577,11 +578,12 @@ __global__ void __launch_bounds__(kPairThreads) matmul_pair_kernel(const __grid_
         }
       }
     }
-    if (lane == 0) bulk_wait_all();
+    if (lane == 0) bulk_wait_read<0>();
   }
   __syncwarp();
   tc_fence_before();
-  cluster.sync();  // neither leaves while the other reads its memory or signals it
+  __syncthreads();
+  cluster_part();  // neither leaves while the other reads its memory or signals it
   tc_fence_after();
   if (warp == 1) tmem_release<2>(tmem, 512);
   if (abort_flag && tid == 0) report_timeout(p.status);
