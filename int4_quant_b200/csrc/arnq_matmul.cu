@@ -65,14 +65,18 @@ constexpr int kStatic = 2048;  // the kernels' static shared memory, rounded up
 //
 // Fitted to a B200 (launches back to back, weights from HBM): a CTA of the
 // split kernel takes some 0.45 us a chunk of 128 codes of K alone on its SM and
-// 0.7 beside another (with plain loads 0.005 us a row of the chunk), streams at 5.5 TB/s altogether, and has 3.5 us of fixed
-// cost plus 0.035 us a token of the tile for the exchange of partial sums; a
-// CTA pair 0.32 us a chunk and 8 us.  Measured, us, split / pair:
-//   n x k          m = 1        64           128          256          333
-//   4096 x 4096    6.7 / 17.5   9.7 / 17.7   12.8 / 18.1  18.6 / 18.2  19.2 / 18.6
-//   5120 x 7168    11.8 / 26.1  14.5 / 26.3  19.3 / 26.6  29.3 / 26.8  36.1 / 27.0
-//   16384 x 4096   16.3 / 23.5  19.5 / 20.1  23.1 / 20.6  34.0 / 21.0  53 / 31
-//   4096 x 16384   18.3 / 49.7  20.3 / 49.8  24.3 / 50.2  29.9 / 50.4  39.1 / 50.4
+// 0.7 beside another (with plain loads 0.005 us a row of the chunk), streams at
+// 5.5 TB/s altogether, and has 2.5 us of fixed cost plus 0.025 us a token of the
+// tile for the exchange of partial sums (0.02 without); a CTA pair 0.315 us a
+// chunk and 6.5 us.  Of 48 products the estimate picks the slower kernel twice,
+// by at most 5 %.  Measured, us, split / pair:
+//   n x k          m = 1        64           128          256          512
+//   1024 x 4096    5.3 / 16.2   6.3 / 16.3   7.7 / 16.6   9.3 / 16.7   13.3 / 16.8
+//   4096 x 4096    6.5 / 16.4   9.2 / 16.5   13.2 / 16.9  12.8 / 16.9  14.8 / 17.5
+//   5120 x 7168    10.9 / 24.4  13.0 / 24.5  16.5 / 24.9  23.2 / 25.1  35.0 / 25.4
+//   16384 x 4096   15.6 / 24.5  16.9 / 19.2  19.6 / 19.4  26.3 / 19.8  51.7 / 29.7
+//   4096 x 16384   16.4 / 46.4  18.8 / 46.3  22.5 / 46.6  24.9 / 47.1  38.3 / 47.1
+//   8192 x 1024    4.6 / 10.1   6.8 / 9.2    8.1 / 9.6    10.2 / 9.7   11.1 / 9.9
 struct SplitPlan {
   int tokens, split, stages, per_sm;
   double us;
@@ -118,7 +122,7 @@ SplitPlan plan_split(const MatmulParams &p, bool plain, int sms, int want_tokens
       const double chunk_us = plain ? 0.005 * (128 + tokens) : 0.45;
       double us = rounds * mine * chunk_us * beside;
       if (us < stream_us(p)) us = stream_us(p);
-      us += 3.5 + (split > 1 ? 0.035 : 0.02) * tokens * rounds;
+      us += 2.5 + (split > 1 ? 0.025 : 0.02) * tokens * rounds;
       if (best.split == 0 || us < best.us) best = SplitPlan{tokens, split, stages, per_sm, us};
     }
   }
@@ -127,9 +131,9 @@ SplitPlan plan_split(const MatmulParams &p, bool plain, int sms, int want_tokens
 
 double pair_us(const MatmulParams &p, int pairs) {
   const int64_t tiles = div_up(p.m, 256) * div_up(p.n, 256);
-  const double us = 0.32 * static_cast<double>(div_up(p.k, kTileK)) *
+  const double us = 0.315 * static_cast<double>(div_up(p.k, kTileK)) *
                     static_cast<double>(div_up(tiles, static_cast<int64_t>(pairs)));
-  return 8.0 + (us < stream_us(p) ? stream_us(p) : us);
+  return 6.5 + (us < stream_us(p) ? stream_us(p) : us);
 }
 
 arnq_status launch_split(MatmulParams &p, const SplitPlan &plan, bool plain, int dev, cudaStream_t stream) {
