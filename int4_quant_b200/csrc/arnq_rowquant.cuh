@@ -469,13 +469,8 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
       if (!op.value(row, u, keep[i], slots + i * nt + tid, UPT * nt, v[i])) top32 = __int_as_float(0x7F800000);
       top32 = abs_top8(v[i], top32);
     });
-    if (Op::kReadsSlots) {
-      // the thread's slots have been read once top32 is there: the next row's
-      // copies into them may go out
-      asm volatile("" : "+f"(top32));
-      stage(row + gridDim.x);
-    }
     const float M = block_max(top32, sm.top[parity], nwarps);
+    if (Op::kReadsSlots) stage(row + gridDim.x);  // value() has read them, behind the barrier
     RowRecord &rec = sm.rec[records];
     const int64_t code_bytes = Op::QT == 1 ? n / 2 : n;
     uint8_t *yr = out.y + row * code_bytes;
