@@ -8,16 +8,17 @@ using namespace arnq;
 
 template <class T, int QT, int MODE>
 arnq_status by_upt(const NormsParams &p, int upt, int threads, cudaStream_t s) {
-  if constexpr (MODE == WIDE) {
-    if (p.out.units == upt * threads) {
-      if (upt == 1) return launch_rows<NormsOp<T, QT, MODE, 1, true>>(p, threads, s);
+  if (MODE != WIDE || p.out.units == upt * threads) {
+    if (upt == 1) return launch_rows<NormsOp<T, QT, MODE, 1, true>>(p, threads, s);
+    if constexpr (MODE == WIDE)
       if (upt == 2) return launch_rows<NormsOp<T, QT, MODE, 2, true>>(p, threads, s);
-      if (upt == 4) return launch_rows<NormsOp<T, QT, MODE, 4, true>>(p, threads, s);
-    }
-    if (upt == 2) return launch_rows<NormsOp<T, QT, MODE, 2>>(p, threads, s);
+    if (upt == 4) return launch_rows<NormsOp<T, QT, MODE, 4, true>>(p, threads, s);
   }
-  if (upt == 1) return launch_rows<NormsOp<T, QT, MODE, 1>>(p, threads, s);
-  if (upt == 4) return launch_rows<NormsOp<T, QT, MODE, 4>>(p, threads, s);
+  if constexpr (MODE == WIDE) {
+    if (upt == 1) return launch_rows<NormsOp<T, QT, MODE, 1>>(p, threads, s);
+    if (upt == 2) return launch_rows<NormsOp<T, QT, MODE, 2>>(p, threads, s);
+    if (upt == 4) return launch_rows<NormsOp<T, QT, MODE, 4>>(p, threads, s);
+  }
   return launch_rows<NormsOp<T, QT, MODE, 0>>(p, threads, s);
 }
 template <class T, int QT>
@@ -84,6 +85,7 @@ extern "C" arnq_status arnq_post_norm_add_rms_norm_dynamic_quant(
   const int mode = vec ? WIDE : n % 2 == 0 ? PAIRS : ONES;
   p.out.units = units_of(mode, p.out.n);
   row_threads(p.out.units, mode == WIDE, rows > sms, qt == kQNone ? 288 : 384, &upt, &threads);
+  if (mode != WIDE && upt > 0) p.out.units = upt * threads;  // whole chunks, masked past n
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return dt == ARNQ_BF16 ? by_codes<Bf16>(p, qt, mode, upt, threads, s)
                          : by_codes<Fp16>(p, qt, mode, upt, threads, s);

@@ -373,8 +373,8 @@ __device__ __forceinline__ void settle_rows(Op &op, RowRecord *recs, int count, 
 // Op: struct with
 //   Params, T, MODE (the units' shape), UPT (units per thread held in registers;
 //   0: rows longer than that are read again in every phase), FULL (units fill
-//   the threads exactly: no unit is checked, which lets a thread's units
-//   overlap), QT (code type: 0 INT8, 1 INT4, kQNone), STAGED (inputs staged as above), kInputs
+//   the threads exactly, with units behind the row's end where they are masked:
+//   no unit is checked, which lets a thread's units overlap), QT (code type: 0 INT8, 1 INT4, kQNone), STAGED (inputs staged as above), kInputs
 //   (tensors staged), Keep (what a unit keeps besides its values)
 //   stage(row, u, slot, stride)     issues the copies of a unit
 //   prepare(..., next)              the row's statistics; calls next() when the
