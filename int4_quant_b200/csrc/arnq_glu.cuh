@@ -69,14 +69,14 @@ __device__ __noinline__ double glu64(const uint16_t *gate, const uint16_t *up, c
   return smooth ? in * static_cast<double>(Cvt<T>::f1(*smooth)) : in;
 }
 
-template <class T_, int ACT, int QT_, int MODE_, int UPT_, bool FULL_ = false>
+template <class T_, int ACT, int QT_, int MODE_, int UPT_>
 struct GluOp {
   typedef T_ T;
   typedef GluParams Params;
   static constexpr int QT = QT_, UPT = UPT_, kInputs = 2;
   static constexpr bool kReadsSlots = true;
   static constexpr int MODE = MODE_;
-  static constexpr bool FULL = FULL_, STAGED = MODE_ == WIDE && UPT_ > 0;
+  static constexpr bool STAGED = is_wide(MODE_) && UPT_ > 0;
   static constexpr int kMaxThreads = UPT == 4 ? 512 : 1024, kMinCtas = UPT == 4 ? 2 : 1;
   struct Keep {
     float low;  // the unit's smallest z, at most 0
@@ -88,9 +88,15 @@ struct GluOp {
     return p.x + row * (2 * static_cast<int64_t>(p.out.n));
   }
   __device__ __forceinline__ void stage(int64_t row, int u, uint4 *slot, int stride) const {
-    const uint16_t *r = gate_of(row) + 8 * u;
-    copy16_async(slot, r);
-    copy16_async(slot + stride, r + p.out.n);
+    const bool there = MODE == WIDE || 8 * u < p.out.n;
+    const uint16_t *r = gate_of(row) + (there ? 8 * u : 0);
+    if (MODE == WIDE) {
+      copy16_async(slot, r);
+      copy16_async(slot + stride, r + p.out.n);
+    } else {
+      copy16_async(slot, r, there);
+      copy16_async(slot + stride, r + p.out.n, there);
+    }
   }
   template <class E, class N>
   __device__ __forceinline__ void prepare(RowSmem &, int64_t, Keep *, const uint4 *, int, E &&, int, N &&) {}

@@ -8,22 +8,17 @@ using namespace arnq;
 
 template <class T, int QT, int MODE>
 arnq_status by_upt(const NormsParams &p, int upt, int threads, cudaStream_t s) {
-  if (MODE != WIDE || p.out.units == upt * threads) {
-    if (upt == 1) return launch_rows<NormsOp<T, QT, MODE, 1, true>>(p, threads, s);
-    if constexpr (MODE == WIDE)
-      if (upt == 2) return launch_rows<NormsOp<T, QT, MODE, 2, true>>(p, threads, s);
-    if (upt == 4) return launch_rows<NormsOp<T, QT, MODE, 4, true>>(p, threads, s);
-  }
-  if constexpr (MODE == WIDE) {
-    if (upt == 1) return launch_rows<NormsOp<T, QT, MODE, 1>>(p, threads, s);
+  if (upt == 1) return launch_rows<NormsOp<T, QT, MODE, 1>>(p, threads, s);
+  if constexpr (is_wide(MODE))
     if (upt == 2) return launch_rows<NormsOp<T, QT, MODE, 2>>(p, threads, s);
-    if (upt == 4) return launch_rows<NormsOp<T, QT, MODE, 4>>(p, threads, s);
-  }
-  return launch_rows<NormsOp<T, QT, MODE, 0>>(p, threads, s);
+  if (upt == 4) return launch_rows<NormsOp<T, QT, MODE, 4>>(p, threads, s);
+  if constexpr (MODE != TAIL) return launch_rows<NormsOp<T, QT, MODE, 0>>(p, threads, s);
+  return ARNQ_ERR_PLAN;  // (not reached: rows read again are WIDE)
 }
 template <class T, int QT>
 arnq_status by_mode(const NormsParams &p, int mode, int upt, int threads, cudaStream_t s) {
   if (mode == WIDE) return by_upt<T, QT, WIDE>(p, upt, threads, s);
+  if (mode == TAIL) return by_upt<T, QT, TAIL>(p, upt, threads, s);
   if constexpr (QT != 1)
     if (mode == ONES) return by_upt<T, QT, ONES>(p, upt, threads, s);
   return by_upt<T, QT, PAIRS>(p, upt, threads, s);
@@ -82,10 +77,13 @@ extern "C" arnq_status arnq_post_norm_add_rms_norm_dynamic_quant(
   int dev = 0, sms = 0, upt = 0, threads = 0;
   st = current_device(&dev, &sms);
   if (st != ARNQ_OK) return st;
-  const int mode = vec ? WIDE : n % 2 == 0 ? PAIRS : ONES;
+  int mode = vec ? WIDE : n % 2 == 0 ? PAIRS : ONES;
   p.out.units = units_of(mode, p.out.n);
   row_threads(p.out.units, mode == WIDE, rows > sms, qt == kQNone ? 288 : 384, &upt, &threads);
-  if (mode != WIDE && upt > 0) p.out.units = upt * threads;  // whole chunks, masked past n
+  if (upt > 0 && p.out.units != upt * threads) {  // threads hold units behind the row's end
+    if (mode == WIDE) mode = TAIL;
+    p.out.units = upt * threads;
+  }
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return dt == ARNQ_BF16 ? by_codes<Bf16>(p, qt, mode, upt, threads, s)
                          : by_codes<Fp16>(p, qt, mode, upt, threads, s);

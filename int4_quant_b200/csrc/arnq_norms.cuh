@@ -101,14 +101,14 @@ __device__ __noinline__ double sumsq_cold(const uint16_t *a, const uint16_t *h, 
   return s;
 }
 
-template <class T_, int QT_, int MODE_, int UPT_, bool FULL_ = false>
+template <class T_, int QT_, int MODE_, int UPT_>
 struct NormsOp {
   typedef T_ T;
   typedef NormsParams Params;
   static constexpr int QT = QT_, UPT = UPT_, kInputs = 2;
   static constexpr bool kReadsSlots = false;  // after prepare()
   static constexpr int MODE = MODE_;
-  static constexpr bool FULL = FULL_, STAGED = MODE_ == WIDE && UPT_ > 0;
+  static constexpr bool STAGED = is_wide(MODE_) && UPT_ > 0;
   static constexpr int kMaxThreads = UPT == 4 ? (QT == kQNone ? 288 : 384) : 1024,
                        kMinCtas = UPT == 4 ? (QT == kQNone ? 3 : 2) : 1;
   struct Keep {
@@ -152,9 +152,15 @@ struct NormsOp {
                       : nullptr;
   }
   __device__ __forceinline__ void stage(int64_t row, int u, uint4 *slot, int stride) const {
-    const int64_t off = row * p.out.n + 8 * u;
-    copy16_async(slot, p.h + off);
-    copy16_async(slot + stride, p.x + off);
+    const bool there = MODE == WIDE || 8 * u < p.out.n;
+    const int64_t off = row * p.out.n + (there ? 8 * u : 0);
+    if (MODE == WIDE) {
+      copy16_async(slot, p.h + off);
+      copy16_async(slot + stride, p.x + off);
+    } else {
+      copy16_async(slot, p.h + off, there);
+      copy16_async(slot + stride, p.x + off, there);
+    }
   }
   __device__ __forceinline__ uint4 get_h(int64_t row, int u, const uint4 *slot) const {
     return STAGED ? slot[0] : load_unit<MODE>(p.h + row * p.out.n, u, p.out.n);

@@ -56,24 +56,28 @@ __device__ __forceinline__ void set16(uint4 &w, int j, uint16_t v) {
 
 // A unit is eight elements of a row, held as eight 16-bit halves.  Which ones:
 //   WIDE   8u + j: one 16-byte access (n a multiple of 8, everything aligned)
+//   TAIL   the same for threads that hold more units than the row has: those
+//          behind its end are masked where they are loaded and stored
 //   PAIRS  element pairs 64 apart, the warp's lanes side by side: four 4-byte
 //          (or eight 2-byte) accesses of whole runs (n even)
 //   ONES   elements 32 apart, the lanes side by side (n odd)
-enum : int { WIDE = 0, PAIRS = 1, ONES = 2 };
+enum : int { WIDE = 0, PAIRS = 1, ONES = 2, TAIL = 3 };
+constexpr bool is_wide(int mode) { return mode == WIDE || mode == TAIL; }
 template <int MODE>
 __device__ __forceinline__ int column(int u, int j) {
-  if (MODE == WIDE) return 8 * u + j;
+  if (is_wide(MODE)) return 8 * u + j;
   const int base = (u >> 5) * 256, lane = u & 31;
   return MODE == PAIRS ? base + (j >> 1) * 64 + 2 * lane + (j & 1) : base + j * 32 + lane;
 }
 __host__ __device__ inline int units_of(int mode, int n) {
-  return mode == WIDE ? n / 8 : (n + 255) / 256 * 32;
+  return is_wide(mode) ? n / 8 : (n + 255) / 256 * 32;
 }
 
 // Unit u of a row of n; zeros past the row's end.
 template <int MODE>
 __device__ __forceinline__ uint4 load_unit(const uint16_t *row, int u, int n) {
-  if (MODE == WIDE) return *reinterpret_cast<const uint4 *>(row + 8 * static_cast<int64_t>(u));
+  if (MODE == TAIL && 8 * u >= n) return make_uint4(0u, 0u, 0u, 0u);
+  if (is_wide(MODE)) return *reinterpret_cast<const uint4 *>(row + 8 * static_cast<int64_t>(u));
   const int c = column<MODE>(u, 0);
   const uint16_t *p = row + c;
   uint32_t r[4];
@@ -107,7 +111,8 @@ __device__ __forceinline__ uint4 load_unit(const uint16_t *row, int u, int n) {
 
 template <int MODE>
 __device__ __forceinline__ void store_unit(uint16_t *row, int u, int n, const uint4 &w) {
-  if (MODE == WIDE) {
+  if (is_wide(MODE)) {
+    if (MODE == TAIL && 8 * u >= n) return;
     *reinterpret_cast<uint4 *>(row + 8 * static_cast<int64_t>(u)) = w;
     return;
   }
@@ -129,7 +134,8 @@ __device__ __forceinline__ void store_unit(uint16_t *row, int u, int n, const ui
 // Eight codes (bytes, or nibbles in lo) of unit u of the code row.
 template <int MODE, int QT>
 __device__ __forceinline__ void store_codes(uint8_t *row, int u, int n, uint32_t lo, uint32_t hi) {
-  if (MODE == WIDE) {
+  if (is_wide(MODE)) {
+    if (MODE == TAIL && 8 * u >= n) return;
     if (QT == 0) reinterpret_cast<uint2 *>(row)[u] = make_uint2(lo, hi);
     else reinterpret_cast<uint32_t *>(row)[u] = lo;
     return;
@@ -294,6 +300,12 @@ struct RowOut {
 // itself (16 bytes at a time, asynchronously): slot (tensor, i) of thread tid
 // holds unit tid + i*nt of that tensor.  A thread reads only what it copied,
 // so its own wait is all the synchronisation there is.
+// there: false for a unit behind the row's end (zeros; the address is not read)
+__device__ __forceinline__ void copy16_async(uint4 *dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
 __device__ __forceinline__ void copy16_async(uint4 *dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
@@ -371,11 +383,12 @@ __device__ __forceinline__ void settle_rows(Op &op, RowRecord *recs, int count, 
 }
 
 // Op: struct with
-//   Params, T, MODE (the units' shape), UPT (units per thread held in registers;
-//   0: rows longer than that are read again in every phase), FULL (units fill
-//   the threads exactly, with units behind the row's end where they are masked:
-//   no unit is checked, which lets a thread's units overlap), QT (code type: 0 INT8, 1 INT4, kQNone), STAGED (inputs staged as above), kInputs
-//   (tensors staged), Keep (what a unit keeps besides its values)
+//   Params, T, MODE (the units' shape), UPT (units per thread held in registers,
+//   exactly: units behind the row's end are masked, not branched around, so
+//   that a thread's units overlap; 0: rows longer than that are read again in
+//   every phase), QT (code type: 0 INT8, 1 INT4, kQNone), STAGED (inputs
+//   staged as above), kInputs (tensors staged), Keep (what a unit keeps
+//   besides its values)
 //   stage(row, u, slot, stride)     issues the copies of a unit
 //   prepare(..., next)              the row's statistics; calls next() when the
 //                                   thread's slots have been read, unless
@@ -411,8 +424,7 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
     if (UPT > 0) {
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
-        const int u = tid + i * nt;
-        if (Op::FULL || u < units) f(u, i);
+        f(tid + i * nt, i);
       }
     } else {
       for (int u = tid; u < units; u += nt) f(u, 0);
