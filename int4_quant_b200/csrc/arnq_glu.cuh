@@ -149,6 +149,14 @@ struct GluOp {
     const uint16_t *g = gate_of(row) + c;
     return glu64<T, ACT>(g, g + p.out.n, p.smooth ? p.smooth + c : nullptr);
   }
+  __device__ __forceinline__ bool zero_row(int64_t row, int tid, int nt) const {
+    uint32_t bits = 0u;
+    for (int u = tid; u < p.out.units; u += nt) {
+      const uint4 g = load_unit<MODE>(gate_of(row), u, p.out.n), t = load_unit<MODE>(gate_of(row) + p.out.n, u, p.out.n);
+      bits |= g.x | g.y | g.z | g.w | t.x | t.y | t.z | t.w;
+    }
+    return (bits & 0x7FFF7FFFu) == 0u;
+  }
   __device__ __forceinline__ void save(double *) const {}
   __device__ __forceinline__ void restore(int64_t, const double *) const {}
   // units that may hold the maximum: 2^-13 covers the error for every z >= kLow

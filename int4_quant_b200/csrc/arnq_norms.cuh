@@ -123,8 +123,9 @@ struct NormsOp {
   float bmax;  // max |beta * smooth|
   const uint16_t *gate_row;
   Rms post, pre;
+  bool zero;  // x' is zero throughout
   __device__ __forceinline__ explicit NormsOp(const Params &q)
-      : p(q), bmax(0.f), gate_row(nullptr) {}
+      : p(q), bmax(0.f), gate_row(nullptr), zero(false) {}
 
   __device__ __forceinline__ void setup(RowSmem &sm, int tid, int nt, int nwarps) {
     if (!p.beta) return;
@@ -210,9 +211,15 @@ struct NormsOp {
     }
     uint4 r = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     const bool beyond = !(tmax <= kHuge);  // a product overflowed (0 times it would be NaN), or is NaN
-    if (differ || beyond)
-      r = settle_x<T, MODE>(r, beyond ? make_uint4(~lo[0], ~lo[1], ~lo[2], ~lo[3]) : make_uint4(hi[0], hi[1], hi[2], hi[3]),
-                            get_h(row, u, slot), xw, p.gamma_post, gate_row, post.inv64, u, p.out.n);
+    if (differ || beyond) {
+      const uint4 hw = get_h(row, u, slot);
+      if (!beyond && ((hw.x | hw.y | hw.z | hw.w) & 0x7FFF7FFFu) == 0u && !post.cold)  // (padding) v is x itself
+        r = make_uint4(Cvt<T>::pack(v[0].x, v[0].y), Cvt<T>::pack(v[1].x, v[1].y), Cvt<T>::pack(v[2].x, v[2].y),
+                       Cvt<T>::pack(v[3].x, v[3].y));
+      else
+        r = settle_x<T, MODE>(r, beyond ? make_uint4(~lo[0], ~lo[1], ~lo[2], ~lo[3]) : make_uint4(hi[0], hi[1], hi[2], hi[3]),
+                              hw, xw, p.gamma_post, gate_row, post.inv64, u, p.out.n);
+    }
     unpack<T>(r, keep.f);
     return r;
   }
@@ -253,6 +260,7 @@ struct NormsOp {
                          post.inv64, p.out.n);
       ss = block_sum(ss, sm.sum[2], nwarps);
     }
+    zero = ss == 0.0;
     pre = make_rms(ss, p.inv_n, p.eps, 1.f, cold);
   }
 
@@ -284,6 +292,7 @@ struct NormsOp {
     if (p.smooth) y = __dmul_rn(y, static_cast<double>(Cvt<T>::f1(p.smooth[c])));
     return y;
   }
+  __device__ __forceinline__ bool zero_row(int64_t, int, int) const { return zero && !p.beta; }
   __device__ __forceinline__ void save(double *stat) const {
     stat[0] = post.inv64;
     stat[1] = pre.inv64;

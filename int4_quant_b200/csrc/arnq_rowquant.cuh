@@ -397,6 +397,8 @@ __device__ __forceinline__ void settle_rows(Op &op, RowRecord *recs, int count, 
 //                                   where they have no error bound
 //   value64(row, c)                 one value in fp64, from memory
 //   kReadsSlots                     value() reads the slots, not prepare()
+//   zero_row(row, tid, nt)          whether this thread's part of the row's
+//                                   inputs is zero, and so the row's values
 //   slack(M)                        bound on |value - value64| over the row
 //   sure(row, u, v, thr)            whether the values >= thr of a unit are as
 //                                   near their fp64 values as coarse() takes the
@@ -487,6 +489,12 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
     const int64_t code_bytes = Op::QT == 1 ? n / 2 : n;
     uint8_t *yr = out.y + row * code_bytes;
     const bool wide = !(M >= kTiny && M <= kHuge);
+    if (M == 0.f && __syncthreads_and(op.zero_row(row, tid, nt))) {
+      // ---- a row of zeros (padding)
+      if (tid == 0) out.scale[row] = 0.f;
+      each([&](int u, int) { store_codes<MODE, Op::QT>(yr, u, n, 0u, 0u); });
+      continue;
+    }
     if (wide) {
       // ---- the whole row in fp64
       if (tid == 0) sm.cand = 0ull;

@@ -199,6 +199,24 @@ def test_norms_parameter_products_beyond_binary32(qdtype, n):
     check_norms(c, run_norms(c, qdtype), qdtype)
 
 
+@pytest.mark.parametrize("qdtype", ["int8", "int4"])
+@pytest.mark.parametrize("n", [1024, 520, 1002, 20000])
+def test_padding_rows(qdtype, n):
+    # rows of zeros (of either sign) among others, in every position of a CTA's turn
+    c = norms_case(700, n, seed=20, gate_rows=1, smooth=True)
+    pad = torch.arange(700) % 3 != 1
+    c["h"][pad] = 0
+    c["x"][pad] = -0.0
+    y, scale, x_out = got = run_norms(c, qdtype)
+    check_norms(c, got, qdtype)
+    assert not scale.cpu()[pad].any() and not R.codes_of(y, qdtype)[pad].any()
+    x, s = glu_case(700, n, seed=21)
+    x[pad] = 0
+    check_glu(x, s, "silu", qdtype)
+    x[pad, n:] = 1.0  # an up projection alone
+    check_glu(x, s, "gelu_tanh", qdtype)
+
+
 @pytest.mark.parametrize("alpha", [0.0, 1.0, -0.5, 1e-38, 1e30])
 def test_norms_residual_scale(alpha):
     c = norms_case(4, 264, seed=9, gate_rows=4)
