@@ -65,7 +65,10 @@
  * Kernels that wait on asynchronous copies do so with a time limit (1 s
  * unless a plan sets wait_limit_us); if a wait expires the kernel stops early
  * and records ARNQ_ERR_DEVICE_TIMEOUT in the workspace's status block (see
- * arnq_workspace_status).
+ * arnq_workspace_status).  Two waits of arnq_quant_matmul have no limit of
+ * their own: a CTA waits for the tensor memory (TMEM) it needs, and the CTAs of
+ * a cluster wait for each other.  A CTA that shares its product's sums with
+ * others holds no TMEM while it waits for them.
  */
 #ifndef ARNQ_H
 #define ARNQ_H

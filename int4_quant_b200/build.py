@@ -23,7 +23,7 @@ SOURCES = [os.path.join(SRC_DIR, f) for f in ["arnq_api.cu", "arnq_host.cu", "ar
 DEPS = SOURCES + [os.path.join(SRC_DIR, f) for f in (
     "arnq_kernels.cuh", "arnq_table.h", "arnq_host.h", "arnq_rowquant.cuh",
     "arnq_rowquant_host.h", "arnq_norms.cuh", "arnq_glu.cuh", "arnq_tc.cuh",
-    "arnq_matmul.cuh")] + [
+    "arnq_matmul.cuh", "arnq_matmul_shape.h")] + [
         os.path.join(ROOT, "include", "arnq.h")]
 LIB = os.path.join(PKG, "libarnq.so")
 OBJ_DIR = os.path.join(ROOT, "_build")

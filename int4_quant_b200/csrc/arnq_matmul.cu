@@ -6,6 +6,7 @@
 #include <cstring>
 
 #include "arnq_host.h"
+#include "arnq_matmul_shape.h"
 
 namespace {
 using namespace arnq;
@@ -58,8 +59,8 @@ bool encode_out(CUtensorMap *map, void *y, int64_t m, int64_t n, int out) {
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kSmemLimit = 227 * 1024;
 constexpr int kStatic = 2048;  // the kernels' static shared memory, rounded up
+static_assert(kPairSmem >= kTmemColumns * kSmemPerColumn, "a pair's 512 columns leave room for no other CTA");
 
 // ---- the choice of kernel and split, by estimated time in us
 //
@@ -144,11 +145,8 @@ arnq_status launch_split(MatmulParams &p, const SplitPlan &plan, bool plain, int
   p.stages = plan.stages;
   p.channel_tiles = static_cast<int32_t>(tiles);
   if (tiles * token_tiles * split > INT32_MAX) return ARNQ_ERR_SHAPE;
-  int smem = p.stages * (16384 + p.tokens * 128);
-  if (smem < p.tokens * 512) smem = p.tokens * 512;  // the partial sums lie over the stages
-  smem += 1024;
-  p.tmem_cols = 32;
-  while (p.tmem_cols < static_cast<uint32_t>(p.tokens)) p.tmem_cols *= 2;
+  const int smem = split_smem(p.tokens, p.stages);
+  p.tmem_cols = static_cast<uint32_t>(split_columns(p.tokens));
   if (!plain && !(encode(&p.map_w, p.w, p.n, p.k, 128) && encode(&p.map_x, p.x, p.m, p.k, p.tokens)))
     return ARNQ_ERR_CUDA;
   const void *fn = plain ? reinterpret_cast<const void *>(matmul_split_kernel<true>)

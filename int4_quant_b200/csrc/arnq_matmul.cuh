@@ -150,6 +150,10 @@ __device__ __forceinline__ void load_tile_any(uint32_t dst, const int8_t *base, 
 // CTAs.  Each CTA streams its part of the weights once; the partial sums meet
 // through distributed shared memory, added as integers (any order, same
 // result), each CTA finishing every split-th token.
+// Two waits have no limit of their own: for TMEM, which only CTAs of other
+// launches could hold (see arnq_matmul_shape.h; those of other libraries, which
+// must give it up without waiting for this kernel), and at the cluster's
+// barriers, for CTAs whose own waits are bounded.
 // Warps: 0 copies, 1 MMA and TMEM, 2-5 the epilogue.  With PLAIN, for codes
 // that tensor maps cannot describe (k or the pointers not multiples of 16),
 // warps 2-9 load.
@@ -214,7 +218,7 @@ __global__ void __launch_bounds__(PLAIN ? kPlainThreads : kSplitThreads)
   // for this grid's completion before touching memory).
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // every wait is bounded; whoever gives up tells the others
+  // every wait for copies and MMAs is bounded; whoever gives up tells the others
   auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
     if (mbar_try_wait(smem_addr(bar), parity)) return true;
     if (!abort_flag && mbar_wait_bounded(smem_addr(bar), parity, p.wait_limit_ns)) return true;
@@ -292,10 +296,13 @@ __global__ void __launch_bounds__(PLAIN ? kPlainThreads : kSplitThreads)
     }
     tc_fence_before();
   }
-  cg::cluster_group cluster = cg::this_cluster();
-  cluster.sync();  // (a single CTA is a cluster of one)
+  // TMEM is given back before the cluster's barrier: a CTA that holds some never
+  // waits for another one, which may itself wait for TMEM on its SM.
+  __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_release<1>(tmem, p.tmem_cols);
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();  // (a single CTA is a cluster of one)
   const bool failed = abort_flag != 0;
   if (failed && tid == 0) report_timeout(p.status);
 
@@ -403,8 +410,8 @@ __global__ void __launch_bounds__(kPairThreads) matmul_pair_kernel(const __grid_
   const uint32_t tmem = tmem_slot;
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // every wait is bounded; whoever gives up tells this CTA's others (the peer's
-  // waits run out too)
+  // every wait for copies, MMAs and accumulators is bounded; whoever gives up
+  // tells this CTA's others (the peer's waits run out too)
   auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
     if (mbar_try_wait(smem_addr(bar), parity)) return true;
     if (!abort_flag && mbar_wait_bounded(smem_addr(bar), parity, p.wait_limit_ns)) return true;
