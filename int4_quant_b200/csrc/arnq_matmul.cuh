@@ -279,7 +279,8 @@ __global__ void __launch_bounds__(PLAIN ? kPlainThreads : kSplitThreads)
   // ---- partial sums to shared memory: part[t][channel], over the stages
   int32_t *part = reinterpret_cast<int32_t *>(base_ptr);
   if (warp >= 2 && warp < 6) {
-    const bool ok = wait(&done, 0);
+    // one answer for the warp: reading TMEM takes all of its lanes
+    const bool ok = __all_sync(0xFFFFFFFFu, wait(&done, 0));
     tc_fence_after();
     const int quarter = warp & 3;
     if (ok && k_end > k_begin) {

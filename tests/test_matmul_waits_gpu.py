@@ -1,0 +1,40 @@
+"""Products whose waits run out: reported, over in time, and harmless to what
+runs next.  (The held-back bytes are only expected, never copied: every copy and
+MMA that such a call starts ends.)"""
+import time
+
+import pytest
+import torch
+
+import int4_quant_b200 as lib
+from int4_quant_b200 import _abi as A
+from int4_quant_b200 import build as B
+from tests.test_block_matmul_gpu import case, check, planned
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _setup():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    B.build()
+    A.lib()
+    torch.cuda.set_device(0)
+
+
+@pytest.mark.parametrize("tokens,split", [(16, 1), (16, 8), (48, 2), (144, 4), (256, 1), (256, 8)])
+def test_epilogue_and_mma_give_up_together(tokens, split):
+    # their limits run out at the same moment: the epilogue's warps agree on what they saw
+    c = case(300, 512, 2048, seed=tokens + split)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    for limit in (300, 301, 350, 400):
+        ws.zero_()
+        begin = time.monotonic()
+        _, status = planned(c, ws, kernel=1, tokens=tokens, split=split, wait_limit_us=limit,
+                            test_hold_bytes=64)
+        assert status == (A.ARNQ_ERR_DEVICE_TIMEOUT, -1)
+        assert time.monotonic() - begin < 5
+    y, status = planned(c, kernel=1, tokens=tokens, split=split)
+    check(*c, y)
+    assert status[0] == 0
