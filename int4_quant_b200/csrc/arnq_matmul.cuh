@@ -226,20 +226,16 @@ __global__ void __launch_bounds__(PLAIN ? kPlainThreads : kSplitThreads)
     return false;
   };
 
+  int issued = 0;  // (thread 0) chunks whose copies were started
   if (!PLAIN && warp == 0) {
     if (lane == 0) {
-      int i = 0;
-      for (int kc = k_begin; kc < k_end; ++kc, ++i) {
-        const int s = i % stages;
+      for (int kc = k_begin; kc < k_end; ++kc, ++issued) {
+        const int i = issued, s = i % stages;
         if (i >= stages && !wait(&empty[s], ((i / stages) & 1) ^ 1)) break;
         const uint32_t bar = smem_addr(&full[s]), at = base + s * stage_bytes;
         mbar_arrive_expect_tx(bar, stage_bytes + (i == 0 ? p.test_hold : 0u));
         tma_2d(at, &p.map_w, kc * kTileK, static_cast<int>(c0), bar);
         tma_2d(at + 16384u, &p.map_x, kc * kTileK, static_cast<int>(t0), bar);
-      }
-      if (abort_flag) {  // copies still in flight must land before the CTA ends
-        for (int j = i > stages ? i - stages : 0; j < i; ++j)
-          mbar_wait_bounded(smem_addr(&full[j % stages]), (j / stages) & 1, p.wait_limit_ns);
       }
     }
   } else if (warp == 1) {
@@ -258,6 +254,8 @@ __global__ void __launch_bounds__(PLAIN ? kPlainThreads : kSplitThreads)
         mma_commit(smem_addr(&empty[s]));
       }
       mma_commit(smem_addr(&done));
+      // whoever gave up: MMAs still at work must end before TMEM is freed
+      mbar_wait_bounded(smem_addr(&done), 0, p.wait_limit_ns);
     }
   } else if (PLAIN && warp >= 2) {
     const int lt = tid - 64;
@@ -302,6 +300,9 @@ __global__ void __launch_bounds__(PLAIN ? kPlainThreads : kSplitThreads)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_release<1>(tmem, p.tmem_cols);
+  if (abort_flag && tid == 0)  // copies still in flight must land before the CTA ends
+    for (int j = issued > stages ? issued - stages : 0; j < issued; ++j)
+      mbar_wait_bounded(smem_addr(&full[j % stages]), (j / stages) & 1, p.wait_limit_ns);
   cg::cluster_group cluster = cg::this_cluster();
   cluster.sync();  // (a single CTA is a cluster of one)
   const bool failed = abort_flag != 0;
@@ -428,12 +429,12 @@ __global__ void __launch_bounds__(kPairThreads) matmul_pair_kernel(const __grid_
     *c0 = in / size * 256;
   };
 
+  // (thread 0) the next stage, its round's parity, stages filled so far; both CTAs'
+  // copies complete on the first one's barrier
+  int s = 0, filled = 0;
+  uint32_t round = 0;
   if (warp == 0) {
     if (lane == 0) {
-      // stage s, its round's parity; both CTAs' copies complete on the first
-      // one's barrier
-      int s = 0, filled = 0;
-      uint32_t round = 0;
       bool ok = true;
       const uint32_t full0 = peer_addr(smem_addr(&full[0]), 0);
       for (int64_t t = blockIdx.x >> 1; ok && t < tiles; t += pairs) {
@@ -457,18 +458,11 @@ __global__ void __launch_bounds__(kPairThreads) matmul_pair_kernel(const __grid_
           }
         }
       }
-      if (abort_flag && rank == 0)  // copies still in flight must land before the pair ends
-        for (; filled > 0; --filled) {
-          if (s == 0) round ^= 1;
-          s = s == 0 ? kPairStages - 1 : s - 1;
-          mbar_wait_bounded(smem_addr(&full[s]), round, p.wait_limit_ns);
-        }
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       const uint32_t idesc = i8_instr_desc(256, 256);
-      int s = 0, n_tile = 0;
-      uint32_t round = 0;
+      int n_tile = 0;
       bool ok = true;
       for (int64_t t = blockIdx.x >> 1; ok && t < tiles; t += pairs, ++n_tile) {
         const int buf = n_tile & 1;
@@ -492,10 +486,6 @@ __global__ void __launch_bounds__(kPairThreads) matmul_pair_kernel(const __grid_
           }
         }
         if (ok) mma_commit_pair(smem_addr(&acc_full[buf]));
-      }
-      if (abort_flag) {  // MMAs still at work must end before TMEM is freed
-        mma_commit_pair(smem_addr(&drained));
-        mbar_wait_bounded(smem_addr(&drained), 0, p.wait_limit_ns);
       }
     }
   } else {
@@ -591,6 +581,19 @@ __global__ void __launch_bounds__(kPairThreads) matmul_pair_kernel(const __grid_
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (abort_flag && rank == 0) {  // whoever gave up: what is still at work must end
+    if (tid == 32) {              // the MMAs, before TMEM is freed
+      mma_commit_pair(smem_addr(&drained));
+      mbar_wait_bounded(smem_addr(&drained), 0, p.wait_limit_ns);
+    }
+    if (tid == 0)  // the copies, before the pair ends
+      for (; filled > 0; --filled) {
+        if (s == 0) round ^= 1;
+        s = s == 0 ? kPairStages - 1 : s - 1;
+        mbar_wait_bounded(smem_addr(&full[s]), round, p.wait_limit_ns);
+      }
+    __syncwarp();
+  }
   cluster_part();  // neither leaves while the other reads its memory or signals it
   tc_fence_after();
   if (warp == 1) tmem_release<2>(tmem, 512);

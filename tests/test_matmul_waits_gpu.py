@@ -38,3 +38,28 @@ def test_epilogue_and_mma_give_up_together(tokens, split):
     y, status = planned(c, kernel=1, tokens=tokens, split=split)
     check(*c, y)
     assert status[0] == 0
+
+
+@pytest.mark.parametrize("k", [128, 512, 4096])
+@pytest.mark.parametrize("kw", [dict(kernel=1, tokens=16, split=1), dict(kernel=1, tokens=256, split=1),
+                                dict(kernel=2)])
+def test_products_right_behind_one_that_gave_up(kw, k):
+    # the copies are all started before the limit runs out (k = 128, 512) or not (4096);
+    # nothing of the call is still at work when the next ones take its place
+    c = case(600, 1024, k, seed=k)
+    x, sx, w, sw, _ = c
+    ref = lib.quant_matmul(x, sx, w, sw)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    held = A.arnq_matmul_plan(wait_limit_us=500, test_hold_bytes=64, **kw)
+    y = torch.empty(600, 1024, dtype=torch.float32, device="cuda")
+    torch.cuda.synchronize()
+    after = []
+    for _ in range(3):
+        st = A.arnq_quant_matmul_planned(x, sx, w, sw, None, 600, 1024, k, A.ARNQ_FP32, y, ws, 256,
+                                         torch.cuda.current_stream(), held)
+        assert st == A.ARNQ_OK
+        after += [lib.quant_matmul(x, sx, w, sw) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert lib.workspace_status(ws) == (A.ARNQ_ERR_DEVICE_TIMEOUT, -1)
+    for v in after:
+        assert torch.equal(v, ref)
