@@ -458,6 +458,13 @@ __global__ void __launch_bounds__(kPairThreads) matmul_pair_kernel(const __grid_
           }
         }
       }
+      // the last stages' MMAs signal both CTAs too: neither leaves before
+      uint32_t r = round;
+      for (int j = filled, e = s; ok && j > 0; --j) {
+        if (e == 0) r ^= 1;
+        e = e == 0 ? kPairStages - 1 : e - 1;
+        ok = wait(&empty[e], r);
+      }
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
@@ -516,7 +523,9 @@ __global__ void __launch_bounds__(kPairThreads) matmul_pair_kernel(const __grid_
         int32_t r[32];
         tmem_ld32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * 256 + col, r);
         tmem_ld_wait();
-        if (col == 224) {  // this warp has read its part of the tile
+        // this warp has read its part of the tile (said only where a later tile
+        // waits for it: a signal that nobody waits for may reach a CTA that has left)
+        if (col == 224 && t + 2 * pairs < tiles) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(peer_addr(smem_addr(&acc_empty[buf]), 0));
@@ -583,7 +592,7 @@ __global__ void __launch_bounds__(kPairThreads) matmul_pair_kernel(const __grid_
   __syncthreads();
   if (abort_flag && rank == 0) {  // whoever gave up: what is still at work must end
     if (tid == 32) {              // the MMAs, before TMEM is freed
-      mma_commit_pair(smem_addr(&drained));
+      mma_commit_pair(smem_addr(&drained), 1);
       mbar_wait_bounded(smem_addr(&drained), 0, p.wait_limit_ns);
     }
     if (tid == 0)  // the copies, before the pair ends
@@ -594,7 +603,10 @@ __global__ void __launch_bounds__(kPairThreads) matmul_pair_kernel(const __grid_
       }
     __syncwarp();
   }
-  cluster_part();  // neither leaves while the other reads its memory or signals it
+  // neither leaves while the other reads its memory or signals it; signals are all
+  // waited for, unless a wait ran out: the barrier then orders them
+  if (abort_flag) cluster_sync();
+  else cluster_part();
   tc_fence_after();
   if (warp == 1) tmem_release<2>(tmem, 512);
   if (abort_flag && tid == 0) report_timeout(p.status);

@@ -72,6 +72,11 @@ __device__ __forceinline__ void cluster_part() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
+// the same, ordering memory
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
@@ -144,12 +149,13 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
       : "memory");
 }
-// the same for a pair: on the barrier at this address in both of its CTAs
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+// the same for a pair: on the barrier at this address in the CTAs of `ctas` (bit i:
+// CTA i), by default both
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar, int ctas = 3) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           bar),
-      "h"(static_cast<uint16_t>(3))
+      "h"(static_cast<uint16_t>(ctas))
       : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() {

@@ -63,3 +63,27 @@ def test_products_right_behind_one_that_gave_up(kw, k):
     assert lib.workspace_status(ws) == (A.ARNQ_ERR_DEVICE_TIMEOUT, -1)
     for v in after:
         assert torch.equal(v, ref)
+
+
+@pytest.mark.parametrize("m", [256, 512, 768, 300, 1100])
+@pytest.mark.parametrize("n", [256 * 73, 256 * 74, 256 * 75])
+@pytest.mark.parametrize("k", [128, 1024])
+def test_signals_between_the_pairs_ctas_at_their_end(m, n, k):
+    # one to five tiles a pair, the next kernel's barriers right behind them in the same memory
+    c, d = case(m, n, k, seed=1), case(16, 512, 512, seed=2)
+    rc, status = planned(c, kernel=2)
+    check(*c, rc)
+    rd = lib.quant_matmul(*d[:4])
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    x, sx, w, sw, _ = c
+    plan, ys, others = A.arnq_matmul_plan(kernel=2), [], []
+    for _ in range(6):
+        ys.append(torch.empty(m, n, dtype=torch.float32, device="cuda"))
+        st = A.arnq_quant_matmul_planned(x, sx, w, sw, None, m, n, k, A.ARNQ_FP32, ys[-1], ws, 256,
+                                         torch.cuda.current_stream(), plan)
+        assert st == A.ARNQ_OK
+        others.append(lib.quant_matmul(*d[:4]))
+    torch.cuda.synchronize()
+    assert status[0] == 0 and lib.workspace_status(ws)[0] == 0
+    for y, o in zip(ys, others):
+        assert torch.equal(y, rc) and torch.equal(o, rd)
