@@ -402,7 +402,8 @@ __device__ __forceinline__ void settle_rows(Op &op, RowRecord *recs, int count, 
 //   slack(M)                        bound on |value - value64| over the row
 //   sure(row, u, v, thr)            whether the values >= thr of a unit are as
 //                                   near their fp64 values as coarse() takes the
-//                                   row's maximum to be
+//                                   row's maximum to be; else the whole row is
+//                                   decided in fp64
 //   coarse(keep, inv)               bound on the error of a unit's quotients, that
 //                                   of the binary32 scale included
 //   save(stat), restore(row, stat)  what value64() needs of the row
@@ -521,8 +522,11 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
       each([&](int u, int i) {
         if (UPT == 0) op.value(row, u, keep[i], slots, 0, v[i]);
         if (abs_max8(v[i]) < M - 2.f * op.slack(M)) return;
-        const int at = atomicAdd(&rec.tops, op.sure(row, u, v[i], M - 2.f * op.slack(M)) ? 1 : kMaxCap + 1);
+        const bool sure = op.sure(row, u, v[i], M - 2.f * op.slack(M));
+        const int at = atomicAdd(&rec.tops, sure ? 1 : kMaxCap + 1);
         if (at < kMaxCap) rec.top[at] = static_cast<uint16_t>(u);
+        // a scale that coarse() does not cover: every code is decided in fp64
+        if (!sure) atomicAdd(&rec.units, kListCap + 1);
       });
     }
     if (tid == 0) {
