@@ -16,6 +16,12 @@
 // 1e8 it and its error are far below what a row's maximum of at least kTiny
 // (1e-18) can tell from zero; a row with a larger factor there is computed in
 // fp64.
+// The binary32 values are 2^64 times the true ones (the sigmoid is formed so, at
+// no cost): gate * sigmoid then never falls below the normal range, where it would
+// lose bits that a large up value lifts, and a gate beyond 2^64 overflows and sends
+// its row to fp64.  up * smooth may fall below it in bf16 and lose up to 2^-150; times
+// less than 2^128 that is 2^-22 at most, a quarter of 2^-24 of a maximum of at least
+// kTiny (18.4 so scaled), and goes into the bounds' spare unit.
 #pragma once
 
 #include "arnq_rowquant.cuh"
@@ -23,6 +29,7 @@
 namespace arnq {
 
 constexpr float kLow = -80.f;
+constexpr float kValueScale = 18446744073709551616.f;  // 2^64
 
 enum : int { ACT_SILU = 0, ACT_GELU_TANH = 1 };
 
@@ -75,6 +82,7 @@ struct GluOp {
   typedef GluParams Params;
   static constexpr int QT = QT_, UPT = UPT_, kInputs = 2;
   static constexpr bool kReadsSlots = true;
+  static constexpr float kLeast = kTiny * kValueScale;
   static constexpr int MODE = MODE_;
   static constexpr bool STAGED = is_wide(MODE_) && UPT_ > 0;
   static constexpr int kMaxThreads = UPT == 4 ? 512 : 1024, kMinCtas = UPT == 4 ? 2 : 1;
@@ -127,17 +135,18 @@ struct GluOp {
       float2 s[4];
       unpack<T>(load_unit<MODE>(p.smooth, u, p.out.n), s);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) t[k] = __fmul2_rn(t[k], s[k]);  // exact
+      for (int k = 0; k < 4; ++k) t[k] = __fmul2_rn(t[k], s[k]);  // exact in the normal range
     }
     float low = 0.f;
-    const float2 l = make_float2(-1.44269504088896f, -1.44269504088896f), one = make_float2(1.f, 1.f);
+    const float2 l = make_float2(-1.44269504088896f, -1.44269504088896f),
+                 unit = make_float2(1.f / kValueScale, 1.f / kValueScale);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      // g * sigmoid(z) * u * smooth, exp(-z) = 2^(-z log2 e)
+      // g * sigmoid(z) * u * smooth times 2^64, exp(-z) = 2^(-z log2 e)
       const float2 z = arg2(g[k]);
       asm("min.f32 %0, %1, %2, %3;" : "=f"(low) : "f"(z.x), "f"(z.y), "f"(low));
       const float2 y = __fmul2_rn(z, l);
-      const float2 e = __fadd2_rn(make_float2(exp2_approx(y.x), exp2_approx(y.y)), one);
+      const float2 e = __ffma2_rn(make_float2(exp2_approx(y.x), exp2_approx(y.y)), unit, unit);
       v[k] = __fmul2_rn(__fmul2_rn(g[k], make_float2(rcp_approx(e.x), rcp_approx(e.y))), t[k]);
     }
     keep.low = low;

@@ -107,6 +107,7 @@ struct NormsOp {
   typedef NormsParams Params;
   static constexpr int QT = QT_, UPT = UPT_, kInputs = 2;
   static constexpr bool kReadsSlots = false;  // after prepare()
+  static constexpr float kLeast = kTiny;
   static constexpr int MODE = MODE_;
   static constexpr bool STAGED = is_wide(MODE_) && UPT_ > 0;
   static constexpr int kMaxThreads = UPT == 4 ? (QT == kQNone ? 288 : 384) : 1024,

@@ -393,13 +393,15 @@ __device__ __forceinline__ void settle_rows(Op &op, RowRecord *recs, int count, 
 //   prepare(..., next)              the row's statistics; calls next() when the
 //                                   thread's slots have been read, unless
 //                                   kReadsSlots
-//   value(row, u, keep, ..., v)     a unit's binary32 values; returns false
-//                                   where they have no error bound
+//   value(row, u, keep, ..., v)     a unit's binary32 values, all of a row times the
+//                                   same constant (codes do not depend on it);
+//                                   returns false where they have no error bound
+//   kLeast                          kTiny times that constant
 //   value64(row, c)                 one value in fp64, from memory
 //   kReadsSlots                     value() reads the slots, not prepare()
 //   zero_row(row, tid, nt)          whether this thread's part of the row's
 //                                   inputs is zero, and so the row's values
-//   slack(M)                        bound on |value - value64| over the row
+//   slack(M)                        bound on value()'s error over the row
 //   sure(row, u, v, thr)            whether the values >= thr of a unit are as
 //                                   near their fp64 values as coarse() takes the
 //                                   row's maximum to be; else the whole row is
@@ -489,7 +491,7 @@ __global__ void __launch_bounds__(Op::kMaxThreads, Op::kMinCtas) rowquant_kernel
     RowRecord &rec = sm.rec[records];
     const int64_t code_bytes = Op::QT == 1 ? n / 2 : n;
     uint8_t *yr = out.y + row * code_bytes;
-    const bool wide = !(M >= kTiny && M <= kHuge);
+    const bool wide = !(M >= Op::kLeast && M <= kHuge);
     if (M == 0.f && __syncthreads_and(op.zero_row(row, tid, nt))) {
       // ---- a row of zeros (padding)
       if (tid == 0) out.scale[row] = 0.f;

@@ -58,3 +58,31 @@ def test_glu_maximum_at_a_low_gate(act, lowest, qdtype):
     x = torch.cat([gate, up], 1)
     y, scale = lib.glu_dynamic_quant(x.cuda(), activation=act, qdtype=qdtype)
     same_codes(y, scale, R.glu_in(x, None, act), qdtype)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("qdtype", ["int8", "int4"])
+@pytest.mark.parametrize("n", [1024, 1002, 20000])
+def test_glu_products_below_the_normal_range(n, qdtype, act):
+    # up * smooth falls below 2^-126 (bf16 alone reaches that), a large gate lifts the value
+    # far above it again
+    t = torch.bfloat16
+    g = torch.Generator().manual_seed(2)
+    r = lambda *s: torch.rand(s, generator=g)  # noqa: E731
+    gate = ((r(64, n) + 0.1) * 1e30).to(t)
+    up = ((r(64, n) - 0.5) * 2e-20).to(t)
+    smooth = ((r(n) + 0.1) * 3e-23).to(t)
+    x = torch.cat([gate, up], 1)
+    y, scale = lib.glu_dynamic_quant(x.cuda(), smooth.cuda(), activation=act, qdtype=qdtype)
+    same_codes(y, scale, R.glu_in(x, smooth, act), qdtype)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("size", [1e-38, 3e-39, 1e-40])
+def test_glu_gates_below_the_normal_range(size, act):
+    g = torch.Generator().manual_seed(3)
+    gate = ((torch.rand(64, 1024, generator=g) - 0.5) * 2 * size).to(torch.bfloat16)
+    up = ((torch.rand(64, 1024, generator=g) + 0.1) * 1e37).to(torch.bfloat16)
+    x = torch.cat([gate, up], 1)
+    y, scale = lib.glu_dynamic_quant(x.cuda(), activation=act)
+    same_codes(y, scale, R.glu_in(x, None, act), "int8")
