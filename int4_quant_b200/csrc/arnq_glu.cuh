@@ -68,11 +68,16 @@ template <class T, int ACT>
 __device__ __noinline__ double glu64(const uint16_t *gate, const uint16_t *up, const uint16_t *smooth) {
   const double g = static_cast<double>(Cvt<T>::f1(*gate));
   const double t = static_cast<double>(Cvt<T>::f1(*up));
-  if (g == 0.0 || t == 0.0) return __dmul_rn(g, t);  // (0 times an infinity or NaN is NaN)
-  if (g < -1e300) return __longlong_as_double(0x7FF8000000000000ll);
-  double z = g;
-  if (ACT == ACT_GELU_TANH) z = 1.5957691216057308 * (g + 0.044715 * g * g * g);
-  const double in = g * sigmoid64(z) * t;
+  double in;
+  if (g == 0.0 || t == 0.0) {
+    in = __dmul_rn(g, t);  // (0 times an infinity or NaN is NaN, here and below)
+  } else if (g < -1e300) {
+    in = __longlong_as_double(0x7FF8000000000000ll);
+  } else {
+    double z = g;
+    if (ACT == ACT_GELU_TANH) z = 1.5957691216057308 * (g + 0.044715 * g * g * g);
+    in = g * sigmoid64(z) * t;
+  }
   return smooth ? in * static_cast<double>(Cvt<T>::f1(*smooth)) : in;
 }
 

@@ -86,3 +86,22 @@ def test_glu_gates_below_the_normal_range(size, act):
     x = torch.cat([gate, up], 1)
     y, scale = lib.glu_dynamic_quant(x.cuda(), activation=act)
     same_codes(y, scale, R.glu_in(x, None, act), "int8")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("n", [256, 251, 20000])
+def test_glu_smooth_not_finite_beside_zeros(n, bad, act):
+    # 0 times an infinity or a NaN is NaN: a zero gate, a zero up value, both, neither
+    g = torch.Generator().manual_seed(4)
+    x = torch.randn(5, 2 * n, generator=g).to(torch.bfloat16)
+    smooth = torch.ones(n, dtype=torch.bfloat16)
+    smooth[5] = bad
+    x[0, 5] = 0
+    x[1, n + 5] = -0.0
+    x[2, 5] = x[2, n + 5] = 0
+    x[3] = 0
+    y, scale = lib.glu_dynamic_quant(x.cuda(), smooth.cuda(), activation=act)
+    same_codes(y, scale, R.glu_in(x, smooth, act), "int8")
+    assert torch.isnan(scale[:4]).all() and not torch.isfinite(scale[4])
+    assert not R.codes_of(y, "int8").any()
