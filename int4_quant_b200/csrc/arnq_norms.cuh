@@ -211,10 +211,12 @@ struct NormsOp {
       differ |= lo[k] ^ hi[k];
     }
     uint4 r = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    const bool beyond = !(tmax <= kHuge);  // a product overflowed (0 times it would be NaN), or is NaN
+    // a product overflowed (0 times it would be NaN) or is NaN, or the row is cold
+    // (v may be NaN where 0 met a factor that overflowed, and lo equal hi)
+    const bool beyond = !(tmax <= kHuge) || post.cold;
     if (differ || beyond) {
       const uint4 hw = get_h(row, u, slot);
-      if (!beyond && ((hw.x | hw.y | hw.z | hw.w) & 0x7FFF7FFFu) == 0u && !post.cold)  // (padding) v is x itself
+      if (!beyond && ((hw.x | hw.y | hw.z | hw.w) & 0x7FFF7FFFu) == 0u)  // (padding) v is x itself
         r = make_uint4(Cvt<T>::pack(v[0].x, v[0].y), Cvt<T>::pack(v[1].x, v[1].y), Cvt<T>::pack(v[2].x, v[2].y),
                        Cvt<T>::pack(v[3].x, v[3].y));
       else

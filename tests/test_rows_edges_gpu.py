@@ -105,3 +105,40 @@ def test_glu_smooth_not_finite_beside_zeros(n, bad, act):
     same_codes(y, scale, R.glu_in(x, smooth, act), "int8")
     assert torch.isnan(scale[:4]).all() and not torch.isfinite(scale[4])
     assert not R.codes_of(y, "int8").any()
+
+
+def norms(h, x, gamma_post, gamma, gate=None, beta=None, smooth=None, qdtype="int8", alpha=1.0, eps=1e-6,
+          eps_post=None):
+    """Runs the fused norms; (y, scale, x_out), x_out checked bit by bit and y
+    against the 64-bit form of what follows x_out."""
+    c = lambda t: None if t is None else t.cuda()  # noqa: E731
+    y, scale, x_out = got = lib.post_norm_add_rms_norm_dynamic_quant(
+        c(h), c(x), c(gamma_post), c(gamma), c(beta), c(gate), c(smooth), residual_scale=alpha, eps=eps,
+        eps_post=eps_post, qdtype=qdtype)
+    want = R.norms_x(h, x, gamma_post, gate, alpha, eps if eps_post is None else eps_post)
+    a = x_out.cpu()
+    off = ~((a == want) | (a.isnan() & want.isnan()))
+    assert not off.any(), int(off.sum())
+    v = R.norms_in(a, gamma, beta, smooth, eps)
+    if qdtype is not None:
+        same_codes(y, scale, v, qdtype)
+    return got, v
+
+
+@pytest.mark.parametrize("n", [256, 250, 251, 1000, 20000])
+@pytest.mark.parametrize("qdtype", ["int8", None])
+def test_norms_zeros_beside_a_factor_beyond_binary32(n, qdtype):
+    # h of 1e-39 without eps: residual_scale / Rms(h) overflows binary32, and zeros times it
+    # must not; also behind the row's end
+    t = torch.bfloat16
+    g = torch.Generator().manual_seed(5)
+    h = (torch.randn(6, n, generator=g) * 1e-39).to(t)
+    h[:, 3] = 0
+    h[1, 8:40] = 0
+    h[2, :] = 0
+    h[2, 5] = 1e-38
+    x = torch.randn(6, n, generator=g).to(t)
+    x[4] = 0
+    ones = torch.ones(n, dtype=t)
+    norms(h, x, ones, ones, qdtype=qdtype, eps_post=0.0)
+    norms(h, x, ones, ones, gate=ones[None], qdtype=qdtype, alpha=-3.0, eps=0.0, eps_post=0.0)
