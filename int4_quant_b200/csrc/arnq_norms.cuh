@@ -120,6 +120,11 @@ struct NormsOp {
   // fused multiply-add one of |v|; and the bound's own roundings (v +- e).
   static constexpr float kFactorError = (kExactProducts<T> ? 1.25f : 2.25f) * 5.9604644775390625e-8f;
   static constexpr float kSumError = 2.25f * 5.9604644775390625e-8f;
+  // What G = gamma_post * gate loses below the normal range, at most 2^-150, times
+  // sqrt(ARNQ_MAX_N) < 363, with a factor of two for this constant's own rounding
+  // and the bound's (fp16: G is exact); the sum itself loses up to 2^-150 there.
+  static constexpr float kGateLoss = kExactProducts<T> ? 363.f * 1.401298464324817e-45f : 0.f;
+  static constexpr float kLeastError = 4.f * 1.401298464324817e-45f;
   const Params &p;
   float bmax;  // max |beta * smooth|
   const uint16_t *gate_row;
@@ -197,9 +202,12 @@ struct NormsOp {
       tmax = abs_max3_nan(hg.x, hg.y, tmax);
     }
     // the unit's largest |h G| serves its eight elements; products below the
-    // normal range lose up to 2^-149 each; a cold row has no binary32 bound:
+    // normal range lose up to 2^-149 each, and what G lost is multiplied by h,
+    // which is at most sqrt(n) Rms(h); a cold row has no binary32 bound:
     // everything in fp64
-    const float floor_e = post.cold ? __int_as_float(0x7F800000) : fabsf(post.inv) * 1.1754944e-38f;
+    const float floor_e = post.cold ? __int_as_float(0x7F800000)
+                                    : __fmaf_rn(fabsf(post.inv), 1.1754944e-38f,
+                                                __fmaf_rn(fabsf(p.alpha), kGateLoss, kLeastError));
     const float e = __fmaf_rn(tmax, fabsf(post.inv) * kFactorError, floor_e);
     uint32_t lo[4], hi[4], differ = 0u;
 #pragma unroll

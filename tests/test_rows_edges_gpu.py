@@ -142,3 +142,15 @@ def test_norms_zeros_beside_a_factor_beyond_binary32(n, qdtype):
     ones = torch.ones(n, dtype=t)
     norms(h, x, ones, ones, qdtype=qdtype, eps_post=0.0)
     norms(h, x, ones, ones, gate=ones[None], qdtype=qdtype, alpha=-3.0, eps=0.0, eps_post=0.0)
+
+
+@pytest.mark.parametrize("n", [512, 510, 511, 20000])
+def test_norms_gate_products_below_the_normal_range(n):
+    # gamma_post * gate below 2^-126 (bf16 alone reaches that) beside a large h and residual_scale
+    t = torch.bfloat16
+    g = torch.Generator().manual_seed(6)
+    r = lambda *s: torch.rand(s, generator=g).double() + 1  # noqa: E731
+    h = (torch.randn(4, n, generator=g).double() * 2.0 ** 50).to(t)
+    gamma_post, gate = (r(n) * 2.0 ** -70).to(t), (r(1, n) * 2.0 ** -75).to(t)
+    x = (torch.randn(4, n, generator=g).double() * 2.0 ** -55).to(t)
+    norms(h, x, gamma_post, torch.ones(n, dtype=t), gate=gate, alpha=2.0 ** 90, eps=0.0)
