@@ -107,7 +107,13 @@ struct NormsOp {
   typedef NormsParams Params;
   static constexpr int QT = QT_, UPT = UPT_, kInputs = 2;
   static constexpr bool kReadsSlots = false;  // after prepare()
-  static constexpr float kLeast = kTiny;
+  // The binary32 values of `in` are 2^64 times the true ones in bf16, whose x' / Rms
+  // may otherwise fall below the normal range and lose bits (2^-150) that a large
+  // gamma * smooth lifts.  So scaled they lose 2^-22 at most (times less than 2^128),
+  // a quarter of 2^-24 of a maximum of at least kLeast, within the bounds below, which
+  // count four roundings where there are three.  (fp16 values leave no range.)
+  static constexpr float kValueScale = kExactProducts<T> ? 18446744073709551616.f : 1.f;
+  static constexpr float kLeast = kTiny * kValueScale;
   static constexpr int MODE = MODE_;
   static constexpr bool STAGED = is_wide(MODE_) && UPT_ > 0;
   static constexpr int kMaxThreads = UPT == 4 ? (QT == kQNone ? 288 : 384) : 1024,
@@ -126,7 +132,7 @@ struct NormsOp {
   static constexpr float kGateLoss = kExactProducts<T> ? 363.f * 1.401298464324817e-45f : 0.f;
   static constexpr float kLeastError = 4.f * 1.401298464324817e-45f;
   const Params &p;
-  float bmax;  // max |beta * smooth|
+  float bmax;  // max |beta * smooth|, times kValueScale
   const uint16_t *gate_row;
   Rms post, pre;
   bool zero;  // x' is zero throughout
@@ -142,7 +148,7 @@ struct NormsOp {
       times(v, p.smooth, u);
       b = abs_top8(v, b);
     }
-    bmax = block_max(b, sm.top[1], nwarps);
+    bmax = block_max(b, sm.top[1], nwarps) * kValueScale;
     __syncthreads();  // the slots are used again at once
   }
   __device__ __forceinline__ void times(float2 v[4], const uint16_t *by, int u) const {
@@ -273,6 +279,10 @@ struct NormsOp {
     }
     zero = ss == 0.0;
     pre = make_rms(ss, p.inv_n, p.eps, 1.f, cold);
+    if (kValueScale != 1.f) {
+      pre.cold = pre.cold || !(pre.inv <= 1e30f / kValueScale);
+      pre.inv *= kValueScale;
+    }
   }
 
   __device__ __forceinline__ bool value(int64_t row, int u, Keep &keep, const uint4 *, int, float2 v[4]) const {
@@ -280,15 +290,23 @@ struct NormsOp {
     float2 G[4], B[4];
     unpack<T>(load_unit<MODE>(p.gamma, u, p.out.n), G);
     times(G, p.smooth, u);
-    const float2 r = make_float2(pre.inv, pre.inv);
+    const float2 r = make_float2(pre.inv, pre.inv), up = make_float2(kValueScale, kValueScale),
+                 down = make_float2(1.f / kValueScale, 1.f / kValueScale);
     if (p.beta) {
       unpack<T>(load_unit<MODE>(p.beta, u, p.out.n), B);
       times(B, p.smooth, u);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = __ffma2_rn(__fmul2_rn(keep.f[k], r), G[k], B[k]);
+      for (int k = 0; k < 4; ++k) {
+        if (kValueScale != 1.f) B[k] = __fmul2_rn(B[k], up);
+        v[k] = __ffma2_rn(__fmul2_rn(keep.f[k], r), G[k], B[k]);
+      }
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = __fmul2_rn(__fmul2_rn(keep.f[k], r), G[k]);
+    }
+    if (QT == kQNone && kValueScale != 1.f) {  // (the values themselves are wanted)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = __fmul2_rn(v[k], down);
     }
     return !pre.cold;
   }

@@ -154,3 +154,26 @@ def test_norms_gate_products_below_the_normal_range(n):
     gamma_post, gate = (r(n) * 2.0 ** -70).to(t), (r(1, n) * 2.0 ** -75).to(t)
     x = (torch.randn(4, n, generator=g).double() * 2.0 ** -55).to(t)
     norms(h, x, gamma_post, torch.ones(n, dtype=t), gate=gate, alpha=2.0 ** 90, eps=0.0)
+
+
+@pytest.mark.parametrize("qdtype", ["int8", "int4", None])
+@pytest.mark.parametrize("beta", [False, True])
+@pytest.mark.parametrize("n", [512, 510, 20000])
+def test_norms_values_below_the_normal_range_lifted_again(n, beta, qdtype):
+    # x' / Rms below 2^-126 beside a large gamma * smooth
+    t = torch.bfloat16
+    g = torch.Generator().manual_seed(7)
+    r = lambda *s: torch.randn(s, generator=g).double()  # noqa: E731
+    x, gamma, smooth = r(4, n) * 2.0 ** 50, torch.full((n,), 2.0 ** -70).double(), torch.ones(n).double()
+    x[:, 1::2] = r(4, n // 2) * 2.0 ** -90
+    gamma[1::2] = 2.0 ** 60
+    smooth[1::2] = 2.0 ** 62
+    b = (r(n) * 2.0 ** -20).to(t) if beta else None
+    if beta:
+        smooth[1::2], gamma[1::2] = 1.0, 2.0 ** 122
+    (y, _, _), v = norms(torch.zeros(4, n, dtype=t), x.to(t), torch.ones(n, dtype=t), gamma.to(t), beta=b,
+                         smooth=smooth.to(t), qdtype=qdtype, eps=0.0)
+    if qdtype is None:
+        # binary32: the factor, two products and the sum round once each (2^-24), then once to bf16
+        size = v.abs() + (0 if b is None else 2 * b.double().abs() * smooth.to(t).double())
+        assert ((y.cpu().double() - v).abs() <= 2.0 ** -8 * v.abs() + 2.0 ** -21 * size).all()
