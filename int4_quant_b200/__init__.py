@@ -243,8 +243,8 @@ def _on_stream(call, index, stream):
             return call(T.raw_stream(index))
         with T.cuda.device(index):
             return call(T.raw_stream(index))
-    if isinstance(stream, int):
-        stream = T.cuda.ExternalStream(stream, device=index)
+    if isinstance(stream, int):  # (handle 0 is the default stream; an ExternalStream of 0 is a new one)
+        stream = T.cuda.ExternalStream(stream, device=index) if stream else T.cuda.default_stream(index)
     if stream.device.index != index:
         raise ValueError(f"stream is on {stream.device}, not on cuda:{index}")
     with T.cuda.stream(stream):  # (the device too)
