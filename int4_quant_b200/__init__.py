@@ -369,6 +369,8 @@ def post_norm_add_rms_norm_dynamic_quant(h, x, gamma_post, gamma, beta=None, gat
         if gate.dim() < 1 or gate.shape[-1] != n:
             raise ValueError(f"gate must have shape [{n}] or [g, {n}], got {tuple(gate.shape)}")
         gate_rows = gate.numel() // n if n else 0
+        if n and not gate_rows:  # (its address is NULL: no gate)
+            raise ValueError("gate has no rows")
     if qdtype is None:
         q, cshape, cdt = _abi.ARNQ_NO_CODES, shape, dt
     else:

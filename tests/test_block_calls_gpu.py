@@ -57,3 +57,12 @@ def test_the_default_streams_handle_keeps_its_order(op):
             y = call(0)
         torch.cuda.synchronize()
         assert torch.equal(y, call(None))
+
+
+def test_a_gate_of_no_rows_is_refused():
+    # its address is NULL, which stands for no gate
+    x, one = torch.ones(4, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        lib.post_norm_add_rms_norm_dynamic_quant(x, x, one, one, gate=x[:0])
+    with pytest.raises(lib.ArnqError):
+        lib.post_norm_add_rms_norm_dynamic_quant(x, x, one, one, gate=x[:3])
