@@ -17,6 +17,7 @@ operator runs in the library's kernels.
 """
 from __future__ import annotations
 
+import threading
 from typing import Optional, Tuple
 
 from . import _abi
@@ -271,17 +272,82 @@ def _output(given, name, index, shape, dtype):
     return t, t.data_ptr()
 
 
-_status_blocks = {}
+# Status blocks of the calls that only need one: one for each stream, of a slab that a
+# device gets at its first call, zeroed before anything uses it.
+_STATUS_BLOCKS = 256  # a device's; with more streams the oldest one's block is handed on
+_status_slabs = {}    # device -> uint8 [_STATUS_BLOCKS, ARNQ_WORKSPACE_BYTES]
+_status_blocks = {}   # device -> {stream handle: block}, the oldest first
+_status_lock = threading.Lock()
 
 
 def _status_block(index: int, stream: int) -> int:
-    """Address of the workspace of calls that only need the status block."""
-    key = (index, stream)
-    kept = _status_blocks.get(key)
-    if kept is None:
-        ws = workspace(f"cuda:{index}", _abi.ARNQ_WORKSPACE_BYTES, stream)
-        kept = _status_blocks[key] = (ws.data_ptr(), ws)
-    return kept[0]
+    """Address of the status block of a stream's calls."""
+    try:
+        block = _status_blocks[index][stream]
+    except KeyError:
+        block = _new_status_block(index, stream)
+    return _status_slabs[index][1] + block * _abi.ARNQ_WORKSPACE_BYTES
+
+
+def _new_status_block(index, stream):
+    """(On the stream of the call.)"""
+    import torch
+    with _status_lock:
+        if index not in _status_slabs:
+            if torch.cuda.is_current_stream_capturing():
+                # its memory would be the graph's, its zeroing one of the graph's steps
+                raise RuntimeError("the first quant_matmul on a device cannot be captured into a CUDA graph: "
+                                   "call it, or quant_matmul_status, once before")
+            _make_status_slab(index)
+        blocks = _status_blocks[index]
+        if stream not in blocks:
+            blocks[stream] = len(blocks) if len(blocks) < _STATUS_BLOCKS else blocks.pop(next(iter(blocks)))
+        return blocks[stream]
+
+
+def _make_status_slab(index):
+    import torch
+    with torch.cuda.device(index):
+        slab = torch.zeros(_STATUS_BLOCKS, _abi.ARNQ_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+        torch.cuda.current_stream().synchronize()  # other streams use it too
+    _status_slabs[index] = (slab, slab.data_ptr())
+    _status_blocks[index] = {}
+
+
+def quant_matmul_status(device=None, *, stream=None, clear: bool = False) -> Tuple[int, int]:
+    """(code, row) that quant_matmul's kernels recorded on a device (the current
+    one), or on one of its streams (a torch stream or its handle): code is 0, or
+    ARNQ_ERR_DEVICE_TIMEOUT after a wait ran out, with row -1.  Waits for the
+    device's, or the stream's, work.  A captured call records on the stream that
+    it was captured on, whichever stream its graph runs on.  A status stays until
+    it is cleared; clear=True does that.
+    """
+    import torch
+    index = torch.cuda.current_device() if device is None else torch.device(device).index
+    if index is None:
+        index = torch.cuda.current_device()
+    with _status_lock:
+        if index not in _status_slabs:
+            _make_status_slab(index)
+    blocks, handle = _status_slabs[index][0], None
+    with torch.cuda.device(index):
+        if stream is None:
+            torch.cuda.synchronize()
+        else:
+            handle = stream if isinstance(stream, int) else stream.cuda_stream
+            (torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()).synchronize()
+            at = _status_blocks[index].get(handle)
+            blocks = blocks[:0] if at is None else blocks[at:at + 1]
+        found = (_abi.ARNQ_OK, 0)
+        for block in blocks[:, :16].cpu().contiguous():
+            status = workspace_status(block)
+            if status[0] != _abi.ARNQ_OK:
+                found = status
+                break
+        if clear:
+            blocks.zero_()
+            torch.cuda.current_stream().synchronize()
+    return found
 
 
 def quant_matmul(x, scale_x, w, scale_w, bias=None, *, out_dtype=None, stream=None, out=None):
@@ -293,6 +359,10 @@ def quant_matmul(x, scale_x, w, scale_w, bias=None, *, out_dtype=None, stream=No
     them; w: [n, k] int8 (rows are output channels) and scale_w: [n] float32;
     bias: [n] of the output dtype.  out_dtype: torch.bfloat16 (the default),
     float16 or float32; `out` may pass y [..., n] preallocated.
+
+    The kernels' waits are bounded; should one run out (1 s, a device in trouble),
+    part of y is left unwritten and quant_matmul_status says so.  The first call on
+    a device has to be made outside CUDA graph capture.
     """
     T = _torch_cache or _torch()
     _check(x, "x", T.int8)
