@@ -187,19 +187,30 @@ class _Torch:
 
     def __init__(self):
         import torch
-        try:  # torch's own shortcut: a new tensor on the current device in half the time
-            self.empty = torch._C._dynamo.guards._empty_strided_cuda
+
+        def empty(shape, strides, dtype):
+            return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+
+        # Shortcuts of torch's own: not part of its public interface, so each gives way
+        # to the public call where it is missing.
+        C = torch._C
+        try:
+            # a new tensor on the current device in half the time; it goes past torch's
+            # modes, so only where none is active
+            fast = C._dynamo.guards._empty_strided_cuda
+            dispatch, function = C._len_torch_dispatch_stack, C._len_torch_function_stack
+            self.empty = lambda *a: (empty if dispatch() or function() else fast)(*a)
         except AttributeError:
-            self.empty = lambda shape, strides, dtype: torch.empty_strided(
-                shape, strides, dtype=dtype, device="cuda")
+            self.empty = empty
+        # the current device and stream without building objects
+        self.current_device = getattr(C, "_cuda_getDevice", torch.cuda.current_device)
+        self.raw_stream = getattr(C, "_cuda_getCurrentRawStream",
+                                  lambda index: torch.cuda.current_stream(index).cuda_stream)
         self.Tensor = torch.Tensor
         self.int8, self.uint8, self.int32 = torch.int8, torch.uint8, torch.int32
         self.float32, self.bfloat16 = torch.float32, torch.bfloat16
         self.dt = {torch.bfloat16: _abi.ARNQ_BF16, torch.float16: _abi.ARNQ_FP16}
         self.out = {**self.dt, torch.float32: _abi.ARNQ_FP32}
-        self.current_device = torch._C._cuda_getDevice
-        # the current stream's handle without building a Stream object
-        self.raw_stream = torch._C._cuda_getCurrentRawStream
         self.cuda = torch.cuda
 
 

@@ -169,3 +169,50 @@ def test_a_wait_that_ran_out_reaches_the_caller(no_blocks):
     assert lib.quant_matmul_status(stream=here) == (A.ARNQ_ERR_DEVICE_TIMEOUT, -1)
     assert lib.quant_matmul_status(clear=True) == (A.ARNQ_ERR_DEVICE_TIMEOUT, -1)
     assert lib.quant_matmul_status() == (0, 0)
+
+
+def all_calls():
+    c = product()
+    x, one = torch.ones(4, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    return [lib.quant_matmul(*c), *lib.glu_dynamic_quant(x),
+            *lib.post_norm_add_rms_norm_dynamic_quant(x, x, one, one, qdtype="int4")]
+
+
+def test_modes_see_the_outputs():
+    from torch.overrides import TorchFunctionMode
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    class Dispatched(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            seen.append(func(*args, **(kwargs or {})))
+            return seen[-1]
+
+    class Called(TorchFunctionMode):
+        def __torch_function__(self, func, types, args=(), kwargs=None):
+            seen.append(func(*args, **(kwargs or {})))
+            return seen[-1]
+
+    ref = all_calls()
+    for mode in (Dispatched, Called):
+        seen = []
+        with mode():
+            got = all_calls()
+        made = {id(t) for t in seen}
+        assert all(id(t) in made for t in got), mode
+        for a, b in zip(ref, got):
+            assert torch.equal(a, b)
+
+
+def test_without_torchs_private_shortcuts(monkeypatch):
+    ref = all_calls()
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream", "_len_torch_dispatch_stack"):
+        monkeypatch.delattr(torch._C, name)
+    T = lib._Torch()
+    monkeypatch.undo()
+    monkeypatch.setattr(lib, "_torch_cache", T)
+    side = torch.cuda.Stream()
+    assert T.current_device() == 0 and T.raw_stream(0) == torch.cuda.current_stream().cuda_stream
+    with torch.cuda.stream(side):
+        assert T.raw_stream(0) == side.cuda_stream
+    for a, b in zip(ref, all_calls()):
+        assert torch.equal(a, b)
