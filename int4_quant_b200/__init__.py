@@ -301,14 +301,8 @@ def _status_block(index: int, stream: int) -> int:
 
 
 def _new_status_block(index, stream):
-    """(On the stream of the call.)"""
-    import torch
     with _status_lock:
         if index not in _status_slabs:
-            if torch.cuda.is_current_stream_capturing():
-                # its memory would be the graph's, its zeroing one of the graph's steps
-                raise RuntimeError("the first quant_matmul on a device cannot be captured into a CUDA graph: "
-                                   "call it, or quant_matmul_status, once before")
             _make_status_slab(index)
         blocks = _status_blocks[index]
         if stream not in blocks:
@@ -319,6 +313,10 @@ def _new_status_block(index, stream):
 def _make_status_slab(index):
     import torch
     with torch.cuda.device(index):
+        if torch.cuda.is_current_stream_capturing():
+            # its memory would be the graph's, its zeroing one of the graph's steps
+            raise RuntimeError("the first quant_matmul on a device cannot be captured into a CUDA graph: "
+                               "call it, or quant_matmul_status, once before")
         slab = torch.zeros(_STATUS_BLOCKS, _abi.ARNQ_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
         torch.cuda.current_stream().synchronize()  # other streams use it too
     _status_slabs[index] = (slab, slab.data_ptr())
@@ -326,17 +324,24 @@ def _make_status_slab(index):
 
 
 def quant_matmul_status(device=None, *, stream=None, clear: bool = False) -> Tuple[int, int]:
-    """(code, row) that quant_matmul's kernels recorded on a device (the current
-    one), or on one of its streams (a torch stream or its handle): code is 0, or
+    """(code, row) that quant_matmul's kernels recorded on a device (by default the
+    stream's, else the current one), or on one of its streams (a torch stream or its
+    handle): code is 0, or
     ARNQ_ERR_DEVICE_TIMEOUT after a wait ran out, with row -1.  Waits for the
     device's, or the stream's, work.  A captured call records on the stream that
     it was captured on, whichever stream its graph runs on.  A status stays until
     it is cleared; clear=True does that.
     """
     import torch
-    index = torch.cuda.current_device() if device is None else torch.device(device).index
+    own = None if stream is None or isinstance(stream, int) else stream.device.index
+    if device is None:
+        index = own
+    else:  # (an integer, a name or a torch.device)
+        index = device if isinstance(device, int) else torch.device(device).index
     if index is None:
         index = torch.cuda.current_device()
+    if own is not None and own != index:
+        raise ValueError(f"stream is on cuda:{own}, not on cuda:{index}")
     with _status_lock:
         if index not in _status_slabs:
             _make_status_slab(index)

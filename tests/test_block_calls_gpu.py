@@ -216,3 +216,16 @@ def test_without_torchs_private_shortcuts(monkeypatch):
         assert T.raw_stream(0) == side.cuda_stream
     for a, b in zip(ref, all_calls()):
         assert torch.equal(a, b)
+
+
+def test_status_of_a_device_and_a_stream(no_blocks):
+    s = torch.cuda.Stream()
+    lib.quant_matmul(*product(), stream=s)
+    for device in (None, 0, "cuda", "cuda:0", torch.device("cuda", 0)):
+        assert lib.quant_matmul_status(device, stream=s) == (0, 0)
+
+    class Elsewhere:  # (a stream of a second device)
+        device, cuda_stream = torch.device("cuda", 1), s.cuda_stream
+
+    with pytest.raises(ValueError):
+        lib.quant_matmul_status(0, stream=Elsewhere)
