@@ -272,7 +272,8 @@ struct NormsOp {
     ss = block_sum(ss, sm.sum[1], nwarps);
     cold = ss_out_of_range(ss, p.eps);
     if (cold) {
-      const int64_t off = row * p.out.n;  // (x' stored by other threads: a barrier has passed)
+      const int64_t off = row * p.out.n;
+      __syncwarp();  // x' was stored by other threads: of the warp, or in front of block_sum's barrier
       ss = sumsq_cold<T>(p.x_out ? p.x_out + off : nullptr, p.h + off, p.x + off, p.gamma_post, gate_row,
                          post.inv64, p.out.n);
       ss = block_sum(ss, sm.sum[2], nwarps);

@@ -177,3 +177,19 @@ def test_norms_values_below_the_normal_range_lifted_again(n, beta, qdtype):
         # binary32: the factor, two products and the sum round once each (2^-24), then once to bf16
         size = v.abs() + (0 if b is None else 2 * b.double().abs() * smooth.to(t).double())
         assert ((y.cpu().double() - v).abs() <= 2.0 ** -8 * v.abs() + 2.0 ** -21 * size).all()
+
+
+@pytest.mark.parametrize("n", [8, 96, 250, 256])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_norms_small_rows_summed_again(n, in_place):
+    # one warp a row; x' so small or large that its sum of squares is taken again from x_out
+    t = torch.bfloat16
+    g = torch.Generator().manual_seed(8)
+    h = torch.zeros(400, n, dtype=t)
+    x = (torch.randn(400, n, generator=g).double() * 10.0 ** torch.randint(-36, 20, (400, 1), generator=g)).to(t)
+    one = torch.ones(n, dtype=t)
+    d = x.cuda()
+    y, scale, x_out = lib.post_norm_add_rms_norm_dynamic_quant(
+        h.cuda(), d, one.cuda(), one.cuda(), eps=0.0, out={"x_out": d} if in_place else None)
+    assert torch.equal(x_out.cpu(), x)
+    same_codes(y, scale, R.norms_in(x, one, None, None, 0.0), "int8")
