@@ -122,7 +122,8 @@ typedef enum arnq_qdtype {
   ARNQ_INT4 = 1,
   ARNQ_INT4_INT32 = 2,
   ARNQ_NO_CODES = 16 /* arnq_post_norm_add_rms_norm_dynamic_quant only: no codes and no scale,
-                        the normalised row rounded to dtype, [rows, n]                       */
+                        the normalised row, evaluated in binary32 and rounded to dtype,
+                        [rows, n]                                                            */
 } arnq_qdtype;
 
 /* outputMask encoding: ARNQ_MASK_ABSENT means "outputMaskOptional not given";
@@ -219,8 +220,9 @@ ARNQ_API arnq_status arnq_rms_norm_dynamic_quant(const void *x, const void *gamm
  *   bias     [n] out_dt       optional (NULL = 0)
  *   y        [m, n] out_dt (ARNQ_BF16, ARNQ_FP16 or ARNQ_FP32)
  * with n <= ARNQ_MAX_N, k <= ARNQ_MAX_K.  The sum is exact (32-bit integers);
- * it is converted to binary32, scaled and added to in binary32 and rounded once
- * to out_dt (a scale that is NaN or infinite gives what binary32 gives).
+ * it is converted to binary32, multiplied by scale_x[t], then scale_w[c], and added
+ * to in binary32 and rounded once to out_dt (a scale that is NaN or infinite, or a
+ * product that leaves binary32's range on the way, gives what binary32 gives).
  * Deterministic; one launch.  Codes of any alignment are taken; tensor-map
  * copies need k and both code pointers to be multiples of 16.
  * workspace: arnq_workspace_size()'s 256 bytes, status block zero-filled once;
@@ -278,7 +280,8 @@ ARNQ_API arnq_status arnq_quant_matmul_planned(const void *x, const float *scale
  *   beta, smooth   [n] dtype         optional (NULL = 0, 1)
  *   eps_post, eps  finite and >= 0
  *   qdt            code type of y, or ARNQ_NO_CODES: y [rows, n] dtype holds
- *                  input rounded to dtype and scale is not written (may be NULL)
+ *                  input, evaluated in binary32 and rounded to dtype, and scale is
+ *                  not written (may be NULL)
  *   x_out          [rows, n] dtype, optional; may be x (in-place update)
  * Conventions are those of arnq_run: x' is the value an fp64 evaluation gives,
  * rounded once; the x' that was rounded is the one that is normalised; scale

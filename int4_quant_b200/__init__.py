@@ -430,8 +430,8 @@ def post_norm_add_rms_norm_dynamic_quant(h, x, gamma_post, gamma, beta=None, gat
     each channel) or [g, n], where g divides the number of rows: consecutive
     runs of rows/g rows share a row of it (g sequences of equal length, or one
     row for each token).  Returns (y, scale, x_out); y as in
-    add_rms_norm_dynamic_quant, or with qdtype=None `in` rounded to the
-    inputs' dtype and scale None.  eps_post defaults to eps.  `out` may pass
+    add_rms_norm_dynamic_quant, or with qdtype=None `in`, evaluated in binary32
+    and rounded to the inputs' dtype, and scale None.  eps_post defaults to eps.  `out` may pass
     preallocated tensors under the keys y, scale, x_out; x_out may be x.
     """
     T = _torch_cache or _torch()

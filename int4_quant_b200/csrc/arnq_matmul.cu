@@ -69,15 +69,16 @@ static_assert(kPairSmem >= kTmemColumns * kSmemPerColumn, "a pair's 512 columns 
 // 0.7 beside another (with plain loads 0.005 us a row of the chunk), streams at
 // 5.5 TB/s altogether, and has 2.5 us of fixed cost plus 0.025 us a token of the
 // tile for the exchange of partial sums (0.02 without); a CTA pair 0.315 us a
-// chunk and 6.5 us.  Of 48 products the estimate picks the slower kernel twice,
-// by at most 5 %.  Measured, us, split / pair:
+// chunk and 6.5 us.  Of 48 products (the six weights below, m = 1, 16, 64, 128, 192,
+// 256, 384, 512) the estimate picks the slower kernel twice: 512 x 4096 x 4096, by
+// 6 %, and 256 x 8192 x 1024, by 4 %.  Measured, us, split / pair:
 //   n x k          m = 1        64           128          256          512
-//   1024 x 4096    5.3 / 16.2   6.3 / 16.3   7.7 / 16.6   9.3 / 16.7   13.3 / 16.8
-//   4096 x 4096    6.5 / 16.4   9.2 / 16.5   13.2 / 16.9  12.8 / 16.9  14.8 / 17.5
-//   5120 x 7168    10.9 / 24.4  13.0 / 24.5  16.5 / 24.9  23.2 / 25.1  35.0 / 25.4
-//   16384 x 4096   15.6 / 24.5  16.9 / 19.2  19.6 / 19.4  26.3 / 19.8  51.7 / 29.7
-//   4096 x 16384   16.4 / 46.4  18.8 / 46.3  22.5 / 46.6  24.9 / 47.1  38.3 / 47.1
-//   8192 x 1024    4.6 / 10.1   6.8 / 9.2    8.1 / 9.6    10.2 / 9.7   11.1 / 9.9
+//   1024 x 4096    5.6 / 15.6   6.6 / 15.7   8.2 / 16.0   9.7 / 15.9   13.7 / 16.1
+//   4096 x 4096    6.8 / 15.9   9.6 / 15.9   13.5 / 16.2  13.2 / 16.5  18.2 / 17.1
+//   5120 x 7168    11.1 / 23.8  13.6 / 23.4  17.2 / 23.7  23.8 / 24.1  35.1 / 24.6
+//   16384 x 4096   15.5 / 23.9  17.7 / 19.3  19.8 / 19.5  28.2 / 20.2  52.0 / 29.0
+//   4096 x 16384   16.5 / 44.1  18.9 / 43.9  23.4 / 44.1  26.1 / 44.4  38.6 / 44.5
+//   8192 x 1024    4.9 / 10.3   7.4 / 9.1    7.7 / 9.3    9.8 / 9.4    11.6 / 10.4
 struct SplitPlan {
   int tokens, split, stages, per_sm;
   double us;

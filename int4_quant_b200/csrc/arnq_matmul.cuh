@@ -156,7 +156,7 @@ __device__ __forceinline__ void load_tile_any(uint32_t dst, const int8_t *base, 
 // barriers, for CTAs whose own waits are bounded.
 // Warps: 0 copies, 1 MMA and TMEM, 2-5 the epilogue.  With PLAIN, for codes
 // that tensor maps cannot describe (k or the pointers not multiples of 16),
-// warps 2-9 load.
+// warps 2-9 load.  (That variant gets 64 registers and spills 36 bytes.)
 constexpr int kSplitThreads = 192, kPlainThreads = 320;
 constexpr int kSplitMaxStages = 12;
 
@@ -358,12 +358,13 @@ __global__ void __launch_bounds__(PLAIN ? kPlainThreads : kSplitThreads)
 //
 // What bounds it is shared memory: an MMA of 32 codes reads 4 KB of tokens and 8
 // KB of channels in an SM, and its share of the stage's copies writes 8 KB,
-// against 128 bytes a cycle: 160 cycles where the tensor core needs 128.
-// Measured on 8192 x 7168 x 4096: 164-167 us; when it was at 172 us (175 cycles an
-// MMA), with half of the MMAs left out 133 us, with each done twice 266 us (132
-// cycles an MMA).  A pair working on two tiles of tokens with the same
-// channels (6 KB of copies an MMA, 158 cycles) has no second accumulator left
-// to overlap the epilogue with and came to 175 us.
+// against 128 bytes a cycle: some 160 cycles where the tensor core needs 128.
+// Measured on 8192 x 7168 x 4096: 162-165 us, 155 cycles an MMA (the tensor pipe
+// 83 % active), and a thirteenth tile for eight of the 74 pairs; 186 us in the long
+// run, under the power limit.  At an earlier step (172 us, 175 cycles) half of
+// the MMAs left out gave 133 us, each done twice 266 us (132 cycles an MMA); a pair
+// working on two tiles of tokens with the same channels (6 KB of copies an MMA)
+// had no second accumulator left to overlap the epilogue with and came to 175 us.
 // Warps: 0 copies, 1 MMA and TMEM, 2-5 the epilogue: a thread has a token's
 // row, scales it (token scale in a register, channel scales and bias from the
 // warp's shared memory), packs 128 bytes of it into the warp's swizzled buffer

@@ -4,7 +4,8 @@
 //   p  = h / sqrt(mean(h^2) + eps_post) * gamma_post
 //   x' = RN16(x + alpha * gate * p)            (written as xOut)
 //   in = (x' / sqrt(mean(x'^2) + eps) * gamma + beta) * smooth
-//   scale = row_max(|in|) / Q, code = round(in / scale); or RN16(in), no codes
+//   scale = row_max(|in|) / Q, code = round(in / scale); or, without codes, `in` as
+//   binary32 gives it (four roundings at most), rounded to 16 bits
 //
 // x' is decided like the codes: the binary32 sum v = x + h*G*(alpha/Rms(h)),
 // G = gamma_post*gate (exact: two 16-bit values), carries an error of a few

@@ -17,10 +17,11 @@
 // distance from the exact one the bound covers, and the units left to decide
 // are listed in a record.  After sixteen rows, or its last, the CTA settles its
 // records, eight lanes a row for the exact scales, then eight lanes a listed
-// unit for its codes.  (Decided within each row, the maximum's fp64 value and
-// the codes' cost 33 of the 121 us of the gated activation of 4096 x 16384, in
-// latency that every warp of the row waits for; and in line in every unit, out
-// of the instruction cache, the norms of 8192 x 4096 took 217 us instead of 127.)
+// unit for its codes.  (Decided within each row, out of line, they cost latency that
+// every warp of the row waits for: the gated activation of 4096 x 16384 went from 114
+// to 78 us when the records came.  In line in every unit the loop left the
+// instruction cache: norms of 8192 x 4096 217 us, 127 out of line.  Both at earlier
+// steps; now 82 and 77 us.)
 // Rows whose maximum is below kTiny, above kHuge or not finite are computed
 // in fp64 throughout.  A row holding a NaN gets scale NaN, one holding an
 // infinity scale infinity (NaN if both), both with codes 0; an all-zero row
