@@ -285,7 +285,9 @@ ARNQ_API arnq_status arnq_quant_matmul_planned(const void *x, const float *scale
  *   x_out          [rows, n] dtype, optional; may be x (in-place update)
  * Conventions are those of arnq_run: x' is the value an fp64 evaluation gives,
  * rounded once; the x' that was rounded is the one that is normalised; scale
- * and codes are the fp64 evaluation's.  A row whose Rms is 0 (zeros, with
+ * and codes are the fp64 evaluation's, whose own error is some 2^-51: a half-way
+ * point that the formula meets exactly (without eps Rms may be exact) is taken
+ * either way.  A row whose Rms is 0 (zeros, with
  * eps 0) is normalised to zeros.  A row whose inputs hold a NaN or an infinity
  * gets a scale that is NaN or infinite, as the formula has it, and codes 0.
  * The current device's memory; x_out may be x, no other output may overlap an
